@@ -1,8 +1,8 @@
 """The quantised key-value cache: what is measured of it, and its plain form.
 
 Three operators: tokens are quantised as they are written into a paged cache, rows of the cache are read back as
-bf16, and new tokens attend to the cache.  The cache is a uint8 tensor [pages, heads, page_size * token_bytes]; a
-page of one head is a run of 16-token tiles, each
+bf16, and new tokens attend to the cache.  The cache is a uint8 tensor [pages, heads, page_size, token_bytes], in which
+a page of one head is a run of 16-token tiles, each
 
     16 rows of K codes (D * bits / 8 bytes) | 16 rows of V codes | 16 rows of (scale, bias) fp16 pairs,
 
@@ -124,7 +124,7 @@ def prepare(case, seed):
     n = torch.from_numpy(lengths(case)).cuda()
     width = -(-case["longest"] // page)
     pages = B * width + 3
-    cache = torch.zeros(pages, H, page * token_bytes(case), dtype=torch.uint8, device="cuda")
+    cache = torch.zeros(pages, H, page, token_bytes(case), dtype=torch.uint8, device="cuda")
     table = torch.randperm(pages, generator=g, device="cuda")[: B * width].view(B, width)
     # keys have channels that lie off zero, values do not
     shape = (pages * page // TILE, TILE, H, D)
@@ -181,7 +181,7 @@ def run(state):
 def cells(cache, case):
     """Views of the cache: K codes, V codes [pages, heads, tiles, 16, bytes of a row], and pairs [.., 16, bytes of a row's pairs]."""
     rb = row_bytes(case)
-    tiles = cache.unflatten(2, (-1, TILE * token_bytes(case)))
+    tiles = cache.flatten(2).unflatten(2, (-1, TILE * token_bytes(case)))
     return tuple(tiles[..., a:b].unflatten(3, (TILE, -1)) for a, b in ((0, TILE * rb), (TILE * rb, 2 * TILE * rb), (2 * TILE * rb, None)))
 
 
