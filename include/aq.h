@@ -47,6 +47,8 @@
  *   aq_gather_matmul(_grouped) MoE: each token times its routed expert
  *   aq_mxfp4_* / aq_nvfp4_* / aq_mxfp8_*  the block-scaled float modes
  *                              (their own packed layouts, no biases)
+ *   aq_kv_append / aq_kv_read / aq_kv_attention  a paged key-value cache in the
+ *                              affine format: written, read back, attended to
  * Errors: arguments are validated synchronously, before anything is launched;
  * a rejected call launches nothing and returns a non-zero status.  Nothing is
  * thrown across the ABI and no kernel traps.
@@ -479,10 +481,98 @@ aq_status aq_nvfp4_matmul(const uint16_t *x_bf16, int64_t M, int64_t K, const ui
                           const uint8_t *scales, const float *tensor_scale, int64_t N, uint16_t *y_bf16,
                           uint32_t flags, aq_stream_t stream);
 
+/* ---- quantised key-value cache ---------------------------------------------
+ * A paged cache of a decoder layer's keys and values in the affine format of
+ * this library: each cached row (K or V of one token and head, D values) is
+ * quantised as aq_quantize quantises a weight row, in groups of G along D
+ * (metalworking "MLX Quantization", section "Mechanics"), so that what a decode
+ * step streams besides its weights is 4 or 8 bits a value too.
+ *
+ * Layout of `data`: page_size * aq_kv_token_bytes bytes for each of [pages, heads].  A page
+ * of one head is page_size / 16 tiles of 16 tokens, each
+ *   16 rows of K codes (D*bits/8 bytes a row, packed LSB first),
+ *   16 rows of V codes,
+ *   16 rows of fp16 pairs (scale, bias): the row's D/G pairs of K, then of V.
+ * Sequence b's position p lies in page table[b][p / page_size], there in row
+ * p % page_size.  lens[b] is the sequence's length, the rows that a call writes
+ * included.  A position whose table entry lies outside [0, pages), or at or
+ * behind width * page_size, is absent: nothing is written there, it reads as
+ * zeros, attention leaves it out, and AQ_FAULT_BAD_INDEX is set in the device
+ * fault word.  Table entries that no call needs are not read as pages, so they
+ * may hold anything.  What lies behind a sequence's end is never used, so it may
+ * hold anything, NaN scales too.
+ * Supported: bits 4 or 8; D 64, 128 or 256; G 32, 64 or 128, at most D;
+ * page_size a power of two from 16 to 1024; any other -> AQ_ERR_UNSUPPORTED.
+ * heads <= 65535, pages < 2^31, width * page_size < 2^31. */
+typedef struct {
+  void *data; /* device, 16-byte aligned */
+  int64_t pages;
+  int64_t heads; /* KV heads */
+  int32_t page_size;
+  int32_t D;
+  int32_t G;
+  int32_t bits;
+  const int32_t *table; /* device int32 [batch, width] */
+  const int32_t *lens;  /* device int32 [batch] */
+  int64_t batch;        /* sequences (0: the call does nothing) */
+  int64_t width;
+} aq_kv_cache;
+
+/* Bytes of one token of one head, K and V: 2*D*bits/8 + 8*D/G (0 if unsupported). */
+size_t aq_kv_token_bytes(int D, int G, int bits);
+
+/* Writes new tokens' K and V.  Row r of k and v (bf16, `rows` rows of [heads, D];
+ * a row and a head lie row_stride and head_stride elements apart, each a multiple
+ * of 8, D values contiguous) belongs to sequence b with offsets[b] <= r <
+ * offsets[b + 1] (device int32 [batch + 1], not decreasing) and is one of its last
+ * tokens: with n = offsets[b + 1] - offsets[b], row offsets[b] + j goes to
+ * position lens[b] - n + j.  offsets = NULL: rows / batch rows each (rows must be
+ * a multiple of batch).  A row of no sequence, or of a position below 0 (a padded
+ * batch's slot has length 0), is left out.  Bytes are those of aq_quantize for
+ * the row as fp32: inputs must be finite and within fp16's range, else the values
+ * of that row and group are undefined (of no other).  Two sequences must not be
+ * given the same page to write: which of the two is then held is undefined. */
+aq_status aq_kv_append(const aq_kv_cache *cache, const uint16_t *k_bf16, int64_t k_row_stride, int64_t k_head_stride,
+                       const uint16_t *v_bf16, int64_t v_row_stride, int64_t v_head_stride, int64_t rows,
+                       const int32_t *offsets, aq_stream_t stream);
+
+/* Reads rows back: row r of k and v (bf16 [rows, heads, D], contiguous, 16-byte
+ * aligned) = bf16_rn(fp32_rn(code*scale + bias)) of the position that the same
+ * offsets and lens give it in aq_kv_append (offsets[b + 1] - offsets[b] = lens[b]
+ * reads the whole sequence).  Rows of no sequence are left as they were; a row
+ * whose position is below 0 or absent is zeros. */
+aq_status aq_kv_read(const aq_kv_cache *cache, int64_t rows, const int32_t *offsets, uint16_t *k_bf16,
+                     uint16_t *v_bf16, aq_stream_t stream);
+
+/* Attention of each sequence's last `tokens` tokens (one in plain decode, a few
+ * when drafted tokens are verified) over its cached positions, their own
+ * included (so append comes first).  q bf16: element [b][j][hq][d] lies at
+ * b*q_seq_stride + j*q_token_stride + hq*q_head_stride + d (strides multiples of
+ * 8; 16-byte aligned); query head hq uses KV head hq / (q_heads / heads).  Token
+ * j stands at position p = lens[b] - tokens + j and sees positions
+ * max(0, p - window + 1) .. p, or 0 .. p where window is 0:
+ *   out[b][j][hq] = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale * q.k_t - max),
+ *   lse[b][j][hq] = log sum_t exp(scale * q.k_t)   (fp32, optional: NULL)
+ * on the values that the cache holds, code*scale + bias.  A row that sees
+ * nothing (p < 0, or every position absent) gives zeros, and -inf in lse.
+ * out: bf16 [batch, tokens, q_heads, D], contiguous, 16-byte aligned.
+ * Arithmetic: scores from the exact codes and q as fp16 under a power-of-two
+ * factor of its row (exact for elements down to 2^-28 of the row's largest);
+ * softmax weights and all sums in fp32; the product of a weight and a V scale
+ * rounds to fp16 (11 bits).
+ * workspace: aq_kv_attention_workspace_bytes bytes, 16-byte aligned, for partial
+ * results; it needs no preparation and must not be used by another call in flight
+ * (NULL where that size is 0).  Allocates nothing and can be captured in a graph. */
+size_t aq_kv_attention_workspace_bytes(const aq_kv_cache *cache, int64_t tokens, int64_t q_heads);
+aq_status aq_kv_attention(const aq_kv_cache *cache, const uint16_t *q_bf16, int64_t tokens, int64_t q_heads,
+                          int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride, float scale,
+                          int64_t window, uint16_t *out_bf16, float *lse, void *workspace, size_t workspace_bytes,
+                          aq_stream_t stream);
+
 /* Bits of the device fault word. */
 enum {
   AQ_FAULT_WAIT_MASK = 0x1Fu, /* bits 0-4: a kernel gave up a bounded wait and returned early */
-  AQ_FAULT_BAD_INDEX = 0x20u  /* an embedding id or an expert id was out of range */
+  AQ_FAULT_BAD_INDEX = 0x20u  /* an embedding id, an expert id or a page of a cache's table was out of range */
 };
 
 /* Limit, in SM clock cycles, of every bounded wait of the decode kernel (the
@@ -506,8 +596,9 @@ void aq_set_wait_stall(int on);
 
 /* Reads and clears the device-side fault word of the current device: non-zero
  * when a kernel gave up a bounded wait (an mbarrier that never completed) and
- * returned early, its output then invalid (bits 0-4), or when an embedding id
- * or an expert id was out of range (bit 5).  Synchronizes the device. */
+ * returned early, its output then invalid (bits 0-4), or when an embedding id,
+ * an expert id or a page of a cache's table was out of range (bit 5).
+ * Synchronizes the device. */
 aq_status aq_device_fault(uint32_t *fault_word);
 
 #ifdef __cplusplus

@@ -16,7 +16,8 @@ Names mirror the C entry points: ``aq_quantize``, ``aq_quantize_mse``,
 ``aq_nvfp4_dequantize_f32``, ``aq_nvfp4_matmul``, ``aq_nvfp4_packed_bytes``, ``aq_mxfp8_quantize``,
 ``aq_mxfp8_dequantize``, ``aq_mxfp8_dequantize_f32``, ``aq_mxfp8_matmul``, ``aq_mxfp8_packed_bytes``, ``aq_dispatch``,
 ``aq_matmul_ws``, ``aq_matmul_workspace_bytes``, ``aq_packed_words``,
-``aq_packed_bytes``, ``aq_status_string``, ``aq_device_fault``, ``aq_set_wait_limit``, ``aq_set_wait_stall``.
+``aq_packed_bytes``, ``aq_kv_cache``, ``aq_kv_token_bytes``, ``aq_kv_append``, ``aq_kv_read``, ``aq_kv_attention``,
+``aq_kv_attention_workspace_bytes``, ``aq_status_string``, ``aq_device_fault``, ``aq_set_wait_limit``, ``aq_set_wait_stall``.
 """
 from __future__ import annotations
 
@@ -102,6 +103,14 @@ def lib() -> ctypes.CDLL:
             L.aq_nvfp4_matmul.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, ctypes.c_uint32, vp]
             L.aq_matmul_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
             L.aq_matmul_workspace_bytes.restype = u64
+            L.aq_kv_token_bytes.argtypes = [i32, i32, i32]
+            L.aq_kv_token_bytes.restype = u64
+            kvc, f32 = ctypes.POINTER(_KVCache), ctypes.c_float
+            L.aq_kv_append.argtypes = [kvc, vp, i64, i64, vp, i64, i64, i64, vp, vp]
+            L.aq_kv_read.argtypes = [kvc, i64, vp, vp, vp, vp]
+            L.aq_kv_attention.argtypes = [kvc, vp, i64, i64, i64, i64, i64, f32, i64, vp, vp, vp, u64, vp]
+            L.aq_kv_attention_workspace_bytes.argtypes = [kvc, i64, i64]
+            L.aq_kv_attention_workspace_bytes.restype = u64
             L.aq_dispatch.argtypes = [i64, i64, i64, i32, i32]
             L.aq_dispatch.restype = i32
             L.aq_status_string.argtypes = [i32]
@@ -580,4 +589,173 @@ def aq_mxfp8_matmul(x, packed, scales, out: torch.Tensor | None = None, overlap_
         rc = lib().aq_mxfp8_matmul(x.data_ptr(), M, K, packed.data_ptr(), scales.data_ptr(), N, out.data_ptr(), flags,
                                    _stream(x))
     _check(rc, "aq_mxfp8_matmul")
+    return out
+
+
+# ----------------------------------------------------------------------------- quantised key-value cache
+
+class _KVCache(ctypes.Structure):
+    """aq_kv_cache of include/aq.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("D", ctypes.c_int32), ("G", ctypes.c_int32), ("bits", ctypes.c_int32),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("batch", ctypes.c_int64),
+                ("width", ctypes.c_int64)]
+
+
+def aq_kv_token_bytes(D: int, G: int, bits: int) -> int:
+    return int(lib().aq_kv_token_bytes(D, G, bits))
+
+
+def aq_kv_cache(pages: int, heads: int, page_size: int, D: int, G: int, bits: int, device="cuda") -> torch.Tensor:
+    """A zeroed cache, uint8 [pages, heads, page_size, aq_kv_token_bytes(D, G, bits)].  A page of one head is laid out
+    in tiles of 16 tokens (include/aq.h), so the last two dimensions only count its bytes."""
+    tb = aq_kv_token_bytes(D, G, bits)
+    if tb == 0:
+        raise AqError(AQ_ERR_UNSUPPORTED, "aq_kv_cache")
+    if min(pages, heads, page_size) <= 0:
+        raise ValueError("pages, heads and page_size must be positive")
+    return torch.zeros((pages, heads, page_size, tb), dtype=torch.uint8, device=device)
+
+
+def _need_index(t: torch.Tensor, name: str, dev: torch.device, ndim: int) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != ndim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {ndim}-D int32 tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on the cache's device")
+
+
+def _kv(cache, table, lens, D: int, G: int, bits: int) -> _KVCache:
+    _need(cache, "cache", _BYTE, 4)
+    _need_index(table, "table", cache.device, 2)
+    _need_index(lens, "lens", cache.device, 1)
+    batch, width = table.shape
+    if lens.shape[0] != batch:
+        raise ValueError("table and lens disagree on the number of sequences")
+    pages, heads, page_size, held = cache.shape
+    tb = lib().aq_kv_token_bytes(D, G, bits)
+    if tb == 0:
+        raise AqError(AQ_ERR_UNSUPPORTED, "a key-value cache")
+    if held != tb:
+        raise ValueError(f"a token of the cache has {held} bytes, one of D = {D}, G = {G}, {bits} bits has {tb}")
+    return _KVCache(cache.data_ptr(), pages, heads, page_size, D, G, bits, table.data_ptr(), lens.data_ptr(), batch,
+                    width)
+
+
+def _need_rows(t: torch.Tensor, name: str, dev: torch.device, shape) -> None:
+    """bf16 of this shape, strided, its last dimension contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on the cache's device")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _step(t: torch.Tensor, i: int) -> int:
+    """Stride of a dimension; a dimension of one entry has none that counts."""
+    return t.stride(i) if t.shape[i] > 1 else 0
+
+
+def _need_offsets(offsets, dev: torch.device, batch: int, rows: int) -> int:
+    if offsets is None:
+        if batch and rows % batch:
+            raise ValueError("without offsets every sequence has as many rows: rows must be a multiple of the batch")
+        return 0
+    _need_index(offsets, "offsets", dev, 1)
+    if offsets.shape[0] != batch + 1:
+        raise ValueError("offsets must have one entry more than there are sequences")
+    return offsets.data_ptr()
+
+
+def aq_kv_append(cache, k, v, table, lens, G: int, bits: int, offsets: torch.Tensor | None = None) -> None:
+    """Quantise new tokens' k, v (bf16 [rows, heads, D], strided) into the cache.
+
+    table int32 [batch, width]: the pages of each sequence; lens int32 [batch]: lengths with the new tokens counted;
+    offsets int32 [batch + 1]: rows offsets[b] .. offsets[b + 1] - 1 are the last tokens of sequence b (None: as many
+    rows for each).  See aq_kv_append in include/aq.h."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [rows, heads, D]")
+    rows, _, D = k.shape
+    c = _kv(cache, table, lens, D, G, bits)
+    dev = cache.device
+    _need_rows(k, "k", dev, (rows, c.heads, D))
+    _need_rows(v, "v", dev, (rows, c.heads, D))
+    off = _need_offsets(offsets, dev, c.batch, rows)
+    if rows == 0:
+        return
+    with _on(dev):
+        rc = lib().aq_kv_append(c, k.data_ptr(), _step(k, 0), _step(k, 1), v.data_ptr(), _step(v, 0), _step(v, 1),
+                                rows, off, _stream(cache))
+    _check(rc, "aq_kv_append")
+
+
+def aq_kv_read(cache, table, lens, rows: int, D: int, G: int, bits: int, offsets: torch.Tensor | None = None, out=None):
+    """-> (k, v), bf16 [rows, heads, D]: what the cache holds for the last tokens of each sequence, laid out by
+    offsets as in aq_kv_append.  out: a (k, v) to write into; rows of no sequence stay as they are there."""
+    c = _kv(cache, table, lens, D, G, bits)
+    dev = cache.device
+    off = _need_offsets(offsets, dev, c.batch, rows)
+    shape = (rows, c.heads, D)
+    if out is None:
+        out = (torch.empty(shape, dtype=torch.bfloat16, device=dev), torch.empty(shape, dtype=torch.bfloat16, device=dev))
+    else:
+        for t, name in zip(out, ("k of out", "v of out"), strict=True):
+            _need(t, name, (torch.bfloat16,), 3)
+            _need_rows(t, name, dev, shape)
+    if rows == 0:
+        return out
+    with _on(dev):
+        rc = lib().aq_kv_read(c, rows, off, out[0].data_ptr(), out[1].data_ptr(), _stream(cache))
+    _check(rc, "aq_kv_read")
+    return out
+
+
+def aq_kv_attention_workspace_bytes(cache, table, lens, tokens: int, q_heads: int, D: int, G: int, bits: int) -> int:
+    return int(lib().aq_kv_attention_workspace_bytes(_kv(cache, table, lens, D, G, bits), tokens, q_heads))
+
+
+def aq_kv_attention(q, cache, table, lens, G: int, bits: int, scale: float | None = None, window: int = 0,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None):
+    """Attention of each sequence's last tokens over its cached positions -> bf16, the shape of q.
+
+    q bf16 [batch, tokens, q_heads, D] or [batch, q_heads, D] (one token each), strided; scale: 1/sqrt(D) by default;
+    window: positions a token sees, itself included (0: all); lse fp32 [batch, tokens, q_heads]: written if given;
+    workspace: a CUDA tensor of at least aq_kv_attention_workspace_bytes(...) bytes (None: allocated for the call).
+    See aq_kv_attention in include/aq.h."""
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be [batch, tokens, q_heads, D] or [batch, q_heads, D]")
+    shape = q.shape
+    D, q_heads = shape[-1], shape[-2]
+    tokens = shape[1] if q.dim() == 4 else 1
+    c = _kv(cache, table, lens, D, G, bits)
+    dev = cache.device
+    _need_rows(q, "q", dev, (c.batch, *shape[1:]))
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", (torch.bfloat16,), q.dim())
+        _need_rows(out, "out", dev, shape)
+    lp = 0
+    if lse is not None:
+        _need(lse, "lse", (torch.float32,), q.dim() - 1)
+        if lse.device != dev or lse.shape != shape[:-1]:
+            raise ValueError(f"lse must be {list(shape[:-1])} on the cache's device")
+        lp = lse.data_ptr()
+    if c.batch == 0:
+        return out
+    L = lib()
+    need = L.aq_kv_attention_workspace_bytes(c, tokens, q_heads)
+    if workspace is None:
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    wp, wb = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    with _on(dev):
+        rc = L.aq_kv_attention(c, q.data_ptr(), tokens, q_heads, _step(q, 0), _step(q, 1) if q.dim() == 4 else 0,
+                               _step(q, -2), D**-0.5 if scale is None else scale, window, out.data_ptr(), lp, wp, wb, _stream(cache))
+    _check(rc, "aq_kv_attention")
     return out

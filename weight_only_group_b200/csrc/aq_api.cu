@@ -87,6 +87,10 @@ cudaError_t launch_scatter_rows(const uint16_t *y_sorted, int64_t T, int64_t N, 
 cudaError_t read_and_clear_gather_fault(uint32_t *word);
 cudaError_t launch_mxfp4_tc(const uint16_t *x, int64_t M, int64_t K, const uint32_t *packed, const uint8_t *scales,
                             int64_t N, uint16_t *y, uint32_t flags, cudaStream_t s);
+namespace kv {
+cudaError_t read_and_clear_cache_fault(uint32_t *word);
+cudaError_t read_and_clear_attention_fault(uint32_t *word);
+}  // namespace kv
 }  // namespace aq
 
 namespace {
@@ -733,7 +737,12 @@ aq_status aq_device_fault(uint32_t *fault_word) {
   if (st != AQ_OK) return st;
   uint32_t u = 0;
   st = from_cuda(aq::read_and_clear_qmv5_fault(&u));
-  *fault_word = a | b | c | d | g | h | u;
+  if (st != AQ_OK) return st;
+  uint32_t kc = 0, ka = 0;
+  st = from_cuda(aq::kv::read_and_clear_cache_fault(&kc));
+  if (st != AQ_OK) return st;
+  st = from_cuda(aq::kv::read_and_clear_attention_fault(&ka));
+  *fault_word = a | b | c | d | g | h | u | kc | ka;
   return st;
 }
 

@@ -1,0 +1,79 @@
+// The paged, group-wise quantised key-value cache: its layout and the argument
+// blocks of its kernels (kv_cache.cu writes and reads it, kv_attention.cu
+// attends to it).
+//
+// Layout of the cache: page_size * token_bytes bytes for each of [pages, heads].  A page of
+// one head is a run of page_size / 16 tiles of 16 tokens, each
+//   [16 rows of K codes][16 rows of V codes][16 rows of fp16 (scale, bias) pairs]
+// with D * bits / 8 bytes of codes a row (packed LSB first, as aq_quantize packs
+// a weight row) and a row's D / G pairs of K before its D / G pairs of V.  A tile
+// is what attention consumes at a time, and being contiguous it is one bulk copy.
+#pragma once
+
+#include "common.cuh"
+
+namespace aq {
+namespace kv {
+
+constexpr int kTile = 16;  // tokens of a tile
+
+__host__ __device__ constexpr int row_bytes(int D, int bits) { return D * bits / 8; }
+__host__ __device__ constexpr int meta_bytes(int D, int G) { return 8 * (D / G); }
+__host__ __device__ constexpr int token_bytes(int D, int G, int bits) {
+  return 2 * row_bytes(D, bits) + meta_bytes(D, G);
+}
+__host__ __device__ constexpr int tile_bytes(int D, int G, int bits) { return kTile * token_bytes(D, G, bits); }
+
+// The cache and its sequences as the kernels take them.
+struct Cache {
+  uint8_t *data;
+  const int32_t *table;  // [batch, width]
+  const int32_t *lens;   // [batch]
+  int pages, heads, batch, width;
+  int page_shift;        // log2(page_size)
+};
+
+// The tile of position `pos` in page `page` of head `h`.
+AQ_DEVICE int64_t tile_index(const Cache &c, int page, int h, int pos) {
+  const int in_page = pos & ((1 << c.page_shift) - 1);
+  return ((int64_t(page) * c.heads + h) << (c.page_shift - 4)) + (in_page >> 4);
+}
+
+struct AppendArgs {
+  Cache c;
+  const uint16_t *src[2];        // k, v
+  int64_t row_stride[2], head_stride[2];  // in elements
+  const int32_t *offsets;        // [batch + 1], or null: `rows_per_seq` rows each
+  int64_t rows;
+  int rows_per_seq;
+};
+
+struct ReadArgs {
+  Cache c;
+  uint16_t *dst[2];  // k, v bf16 [rows, heads, D]
+  const int32_t *offsets;
+  int64_t rows;
+  int rows_per_seq;
+};
+
+struct AttentionArgs {
+  Cache c;
+  const uint16_t *q;
+  int64_t q_stride[3];  // sequence, token, head, in elements
+  uint16_t *out;        // bf16 [batch, tokens, q_heads, D]
+  float *lse;           // fp32 [batch, tokens, q_heads], or null
+  int tokens, q_heads, group;  // group: query heads of a KV head
+  int window;           // 0: none
+  float scale;
+  void *workspace;
+};
+
+cudaError_t launch_append(const AppendArgs &a, int D, int G, int bits, cudaStream_t s);
+cudaError_t launch_read(const ReadArgs &a, int D, int G, int bits, cudaStream_t s);
+cudaError_t launch_attention(const AttentionArgs &a, int D, int G, int bits, cudaStream_t s);
+size_t attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t q_heads, int64_t heads, int D, int G, int bits);
+cudaError_t read_and_clear_cache_fault(uint32_t *word);
+cudaError_t read_and_clear_attention_fault(uint32_t *word);
+
+}  // namespace kv
+}  // namespace aq
