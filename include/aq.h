@@ -503,7 +503,7 @@ aq_status aq_nvfp4_matmul(const uint16_t *x_bf16, int64_t M, int64_t K, const ui
  * hold anything, NaN scales too.
  * Supported: bits 4 or 8; D 64, 128 or 256; G 32, 64 or 128, at most D;
  * page_size a power of two from 16 to 1024; any other -> AQ_ERR_UNSUPPORTED.
- * heads <= 65535, pages < 2^31, width * page_size < 2^31. */
+ * heads <= 65535, pages < 2^31, width * page_size <= 2^30. */
 typedef struct {
   void *data; /* device, 16-byte aligned */
   int64_t pages;
@@ -561,9 +561,9 @@ aq_status aq_kv_read(const aq_kv_cache *cache, int64_t rows, const int32_t *offs
  * softmax weights and all sums in fp32; the product of a weight and a V scale
  * rounds to fp16 (11 bits).
  * workspace: aq_kv_attention_workspace_bytes bytes, 16-byte aligned, for partial
- * results; it needs no preparation and must not be used by another call in flight
- * (NULL where that size is 0).  Allocates nothing and can be captured in a graph. */
-size_t aq_kv_attention_workspace_bytes(const aq_kv_cache *cache, int64_t tokens, int64_t q_heads);
+ * results; it needs no preparation and must not be used by another call in flight.
+ * Allocates nothing and can be captured in a graph. */
+size_t aq_kv_attention_workspace_bytes(const aq_kv_cache *cache, int64_t tokens, int64_t q_heads, int64_t window);
 aq_status aq_kv_attention(const aq_kv_cache *cache, const uint16_t *q_bf16, int64_t tokens, int64_t q_heads,
                           int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride, float scale,
                           int64_t window, uint16_t *out_bf16, float *lse, void *workspace, size_t workspace_bytes,

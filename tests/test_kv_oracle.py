@@ -173,12 +173,12 @@ def test_attention_validation():
         assert _attend(c, **kw) == aq.AQ_ERR_ALIGNMENT, kw
     # more units of work than are counted in 32 bits
     assert _attend(_desc(batch=1 << 24, width=1 << 20)) == aq.AQ_ERR_UNSUPPORTED
-    need = aq.lib().aq_kv_attention_workspace_bytes(c, 1, 8)
+    need = aq.lib().aq_kv_attention_workspace_bytes(c, 1, 8, 0)
     if need:
         assert _attend(c, wb=need - 1) == bad
         assert _attend(c, ws=None) == bad
-    assert aq.lib().aq_kv_attention_workspace_bytes(_desc(bits=3), 1, 8) == 0
-    assert aq.lib().aq_kv_attention_workspace_bytes(c, 1, 7) == 0
+    assert aq.lib().aq_kv_attention_workspace_bytes(_desc(bits=3), 1, 8, 0) == 0
+    assert aq.lib().aq_kv_attention_workspace_bytes(c, 1, 7, 0) == 0
 
 
 def test_descriptor_matches_the_header():

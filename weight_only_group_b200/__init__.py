@@ -109,7 +109,7 @@ def lib() -> ctypes.CDLL:
             L.aq_kv_append.argtypes = [kvc, vp, i64, i64, vp, i64, i64, i64, vp, vp]
             L.aq_kv_read.argtypes = [kvc, i64, vp, vp, vp, vp]
             L.aq_kv_attention.argtypes = [kvc, vp, i64, i64, i64, i64, i64, f32, i64, vp, vp, vp, u64, vp]
-            L.aq_kv_attention_workspace_bytes.argtypes = [kvc, i64, i64]
+            L.aq_kv_attention_workspace_bytes.argtypes = [kvc, i64, i64, i64]
             L.aq_kv_attention_workspace_bytes.restype = u64
             L.aq_dispatch.argtypes = [i64, i64, i64, i32, i32]
             L.aq_dispatch.restype = i32
@@ -712,8 +712,9 @@ def aq_kv_read(cache, table, lens, rows: int, D: int, G: int, bits: int, offsets
     return out
 
 
-def aq_kv_attention_workspace_bytes(cache, table, lens, tokens: int, q_heads: int, D: int, G: int, bits: int) -> int:
-    return int(lib().aq_kv_attention_workspace_bytes(_kv(cache, table, lens, D, G, bits), tokens, q_heads))
+def aq_kv_attention_workspace_bytes(cache, table, lens, tokens: int, q_heads: int, D: int, G: int, bits: int,
+                                    window: int = 0) -> int:
+    return int(lib().aq_kv_attention_workspace_bytes(_kv(cache, table, lens, D, G, bits), tokens, q_heads, window))
 
 
 def aq_kv_attention(q, cache, table, lens, G: int, bits: int, scale: float | None = None, window: int = 0,
@@ -747,7 +748,7 @@ def aq_kv_attention(q, cache, table, lens, G: int, bits: int, scale: float | Non
     if c.batch == 0:
         return out
     L = lib()
-    need = L.aq_kv_attention_workspace_bytes(c, tokens, q_heads)
+    need = L.aq_kv_attention_workspace_bytes(c, tokens, q_heads, window)
     if workspace is None:
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)

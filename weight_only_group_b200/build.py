@@ -22,8 +22,8 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libaq.so")
 
 SOURCES = ["aq_api.cu", "quantize.cu", "qmv.cu", "qmv_tc.cu", "qmv_umma.cu", "qmm.cu", "qmm2.cu", "noalloc.cu", "embedding.cu", "mxfp4.cu", "gather.cu",
-           "kv_api.cu", "kv_cache.cu", "kv_attention.cu"]
-HEADERS = ["common.cuh", "tc05.cuh", "kv.cuh"]
+           "kv_api.cu", "kv_cache.cu", "kv_attention4.cu", "kv_attention8.cu"]
+HEADERS = ["common.cuh", "tc05.cuh", "kv.cuh", "kv_attention.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -89,7 +89,8 @@ cudaError_t launch_mxfp4_tc(const uint16_t *x, int64_t M, int64_t K, const uint3
                             int64_t N, uint16_t *y, uint32_t flags, cudaStream_t s);
 namespace kv {
 cudaError_t read_and_clear_cache_fault(uint32_t *word);
-cudaError_t read_and_clear_attention_fault(uint32_t *word);
+cudaError_t read_and_clear_attention_fault4(uint32_t *word);
+cudaError_t read_and_clear_attention_fault8(uint32_t *word);
 }  // namespace kv
 }  // namespace aq
 
@@ -738,11 +739,13 @@ aq_status aq_device_fault(uint32_t *fault_word) {
   uint32_t u = 0;
   st = from_cuda(aq::read_and_clear_qmv5_fault(&u));
   if (st != AQ_OK) return st;
-  uint32_t kc = 0, ka = 0;
+  uint32_t kc = 0, k4 = 0, k8 = 0;
   st = from_cuda(aq::kv::read_and_clear_cache_fault(&kc));
   if (st != AQ_OK) return st;
-  st = from_cuda(aq::kv::read_and_clear_attention_fault(&ka));
-  *fault_word = a | b | c | d | g | h | u | kc | ka;
+  st = from_cuda(aq::kv::read_and_clear_attention_fault4(&k4));
+  if (st != AQ_OK) return st;
+  st = from_cuda(aq::kv::read_and_clear_attention_fault8(&k8));
+  *fault_word = a | b | c | d | g | h | u | kc | k4 | k8;
   return st;
 }
 

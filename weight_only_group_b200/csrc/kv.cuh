@@ -1,5 +1,5 @@
 // The paged, group-wise quantised key-value cache: its layout and the argument
-// blocks of its kernels (kv_cache.cu writes and reads it, kv_attention.cu
+// blocks of its kernels (kv_cache.cu writes and reads it, kv_attention.cuhh
 // attends to it).
 //
 // Layout of the cache: page_size * token_bytes bytes for each of [pages, heads].  A page of
@@ -70,10 +70,11 @@ struct AttentionArgs {
 
 cudaError_t launch_append(const AppendArgs &a, int D, int G, int bits, cudaStream_t s);
 cudaError_t launch_read(const ReadArgs &a, int D, int G, int bits, cudaStream_t s);
-cudaError_t launch_attention(const AttentionArgs &a, int D, int G, int bits, cudaStream_t s);
-size_t attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t q_heads, int64_t heads, int D, int G, int bits);
-cudaError_t read_and_clear_cache_fault(uint32_t *word);
-cudaError_t read_and_clear_attention_fault(uint32_t *word);
+// (4- and 8-bit codes are files of their own, which compile side by side)
+cudaError_t launch_attention4(const AttentionArgs &a, int D, int G, cudaStream_t s);
+cudaError_t launch_attention8(const AttentionArgs &a, int D, int G, cudaStream_t s);
+size_t attention_workspace_bytes4(const AttentionArgs &a, int D, int G);
+size_t attention_workspace_bytes8(const AttentionArgs &a, int D, int G);
 
 }  // namespace kv
 }  // namespace aq

@@ -28,7 +28,7 @@ aq_status check_cache(const aq_kv_cache *c, aq::kv::Cache *out) {
   if (c->pages <= 0 || c->pages > kMaxInt || c->heads <= 0 || c->heads > 65535 || !c->data) return AQ_ERR_INVALID_ARG;
   if (c->batch < 0 || c->batch > kMaxInt) return AQ_ERR_INVALID_ARG;
   if (c->batch > 0) {
-    if (!c->table || !c->lens || c->width <= 0 || c->width > kMaxInt / c->page_size) return AQ_ERR_INVALID_ARG;
+    if (!c->table || !c->lens || c->width <= 0 || c->width > (int64_t(1) << 30) / c->page_size) return AQ_ERR_INVALID_ARG;
     if (!aligned(c->table, 4) || !aligned(c->lens, 4)) return AQ_ERR_ALIGNMENT;
   }
   if (!aligned(c->data, 16)) return AQ_ERR_ALIGNMENT;
@@ -104,25 +104,36 @@ aq_status aq_kv_read(const aq_kv_cache *cache, int64_t rows, const int32_t *offs
   return aq::api_from_cuda(aq::kv::launch_read(a, cache->D, cache->G, cache->bits, stream));
 }
 
-static aq_status check_attention(const aq_kv_cache *cache, int64_t tokens, int64_t q_heads, aq::kv::Cache *c) {
-  const aq_status st = check_cache(cache, c);
+// The sizes that decide on a launch and its workspace: AQ_OK, or the status to return.
+static aq_status check_attention(const aq_kv_cache *cache, int64_t tokens, int64_t q_heads, int64_t window,
+                                 aq::kv::AttentionArgs *a) {
+  const aq_status st = check_cache(cache, &a->c);
   if (st != AQ_OK) return st;
-  if (tokens <= 0 || q_heads <= 0 || tokens > kMaxInt || q_heads > kMaxInt || q_heads % cache->heads != 0)
+  if (tokens <= 0 || q_heads <= 0 || tokens > kMaxInt || q_heads > kMaxInt || q_heads % cache->heads != 0 || window < 0)
     return AQ_ERR_INVALID_ARG;
-  // units of work and query rows are counted in 32 bits
+  // units of work (a chunk of a sequence for each head and each eight rows or fewer) and query rows are counted in 32 bits
   if (cache->batch > 0) {
     const double rows = double(cache->batch) * double(tokens) * double(q_heads);
     const double chunks = double(cache->width) * cache->page_size / aq::kv::kTile + 1.0;
-    if (rows > 2e9 || double(cache->batch) * double(cache->heads) * chunks > 2e9 || rows / 8 * chunks > 2e9)
+    if (rows > 2e9 || double(cache->batch) * double(cache->heads) * chunks > 1e9 || rows / 8 * chunks > 1e9)
       return AQ_ERR_UNSUPPORTED;
   }
+  a->tokens = static_cast<int>(tokens);
+  a->q_heads = static_cast<int>(q_heads);
+  a->group = static_cast<int>(q_heads / cache->heads);
+  a->window = static_cast<int>(window > kMaxInt ? 0 : window);  // (no position is that far away)
   return AQ_OK;
 }
 
-size_t aq_kv_attention_workspace_bytes(const aq_kv_cache *cache, int64_t tokens, int64_t q_heads) {
-  aq::kv::Cache c;
-  if (check_attention(cache, tokens, q_heads, &c) != AQ_OK || c.batch == 0) return 0;
-  return aq::kv::attention_workspace_bytes(c.batch, tokens, q_heads, c.heads, cache->D, cache->G, cache->bits);
+static size_t attention_workspace(const aq_kv_cache *cache, const aq::kv::AttentionArgs &a) {
+  return cache->bits == 4 ? aq::kv::attention_workspace_bytes4(a, cache->D, cache->G)
+                          : aq::kv::attention_workspace_bytes8(a, cache->D, cache->G);
+}
+
+size_t aq_kv_attention_workspace_bytes(const aq_kv_cache *cache, int64_t tokens, int64_t q_heads, int64_t window) {
+  aq::kv::AttentionArgs a;
+  if (check_attention(cache, tokens, q_heads, window, &a) != AQ_OK || a.c.batch == 0) return 0;
+  return attention_workspace(cache, a);
 }
 
 aq_status aq_kv_attention(const aq_kv_cache *cache, const uint16_t *q_bf16, int64_t tokens, int64_t q_heads,
@@ -130,14 +141,11 @@ aq_status aq_kv_attention(const aq_kv_cache *cache, const uint16_t *q_bf16, int6
                           int64_t window, uint16_t *out_bf16, float *lse, void *workspace, size_t workspace_bytes,
                           aq_stream_t stream) {
   aq::kv::AttentionArgs a;
-  aq_status st = check_attention(cache, tokens, q_heads, &a.c);
+  aq_status st = check_attention(cache, tokens, q_heads, window, &a);
   if (st != AQ_OK) return st;
-  if (!std::isfinite(scale) || window < 0) return AQ_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return AQ_ERR_INVALID_ARG;
   if (cache->batch == 0) return AQ_OK;
-  if (!q_bf16 || !out_bf16) return AQ_ERR_INVALID_ARG;
-  const size_t need =
-      aq::kv::attention_workspace_bytes(a.c.batch, tokens, q_heads, a.c.heads, cache->D, cache->G, cache->bits);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return AQ_ERR_INVALID_ARG;
+  if (!q_bf16 || !out_bf16 || !workspace || workspace_bytes < attention_workspace(cache, a)) return AQ_ERR_INVALID_ARG;
   if (!aligned(q_bf16, 16) || !aligned(out_bf16, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
       !stride_ok(q_seq_stride) || !stride_ok(q_token_stride) || !stride_ok(q_head_stride))
     return AQ_ERR_ALIGNMENT;
@@ -148,13 +156,10 @@ aq_status aq_kv_attention(const aq_kv_cache *cache, const uint16_t *q_bf16, int6
   a.q_stride[2] = q_head_stride;
   a.out = out_bf16;
   a.lse = lse;
-  a.tokens = static_cast<int>(tokens);
-  a.q_heads = static_cast<int>(q_heads);
-  a.group = static_cast<int>(q_heads / cache->heads);
-  a.window = static_cast<int>(window > kMaxInt ? 0 : window);  // (no position is that far away)
   a.scale = scale;
   a.workspace = workspace;
-  return aq::api_from_cuda(aq::kv::launch_attention(a, cache->D, cache->G, cache->bits, stream));
+  return aq::api_from_cuda(cache->bits == 4 ? aq::kv::launch_attention4(a, cache->D, cache->G, stream)
+                                            : aq::kv::launch_attention8(a, cache->D, cache->G, stream));
 }
 
 }  // extern "C"

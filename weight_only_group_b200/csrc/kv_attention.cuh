@@ -1,0 +1,938 @@
+// Attention of new tokens over the paged, quantised key-value cache: the kernels.
+// kv_attention4.cu and kv_attention8.cu instantiate them for 4- and 8-bit codes.
+//
+// For a query row and the cached tokens t that it sees,
+//   o_d = sum_t w_t v_td / sum_t w_t,  w_t = exp(scale q.k_t - max),
+// with k and v stored as code * scale + bias in groups along d.  Codes go into the
+// matrix instructions as they are:
+//   q.k_t = sum_g s_tg (sum_{d in g} q_d c_td) + b_tg (sum_{d in g} q_d)
+//   sum_t w_t v_td = sum_t (w_t s_tg) c_td + sum_t w_t b_tg.
+// A code's bits in the low bits of an fp16 are that code times 2^-24 (a subnormal,
+// exact), so unpacking is a mask, and a shift for every second mask; nothing is
+// converted.  The nibble above counts 16 times, which q's fragment (K) and the
+// accumulator's rows (V) take back, both exactly.
+//
+// Bound: the cache's bytes, each read once.  A KV head's few query rows (8 or 16
+// at a time) make mma.sync m16n8k16 the right size: tokens (K) or dimensions (V)
+// are its 16 rows, query rows its 8 columns.  A tcgen05 tile has 128 rows or more
+// and takes its operands from shared or tensor memory, so each code would be
+// unpacked into memory once more for work that is a few percent of the pipe.
+//
+// Work is cut by the cache's bytes, not by sequences: the sequences' chunks (of
+// kCT tiles of 16 tokens) are counted, heads and row tiles included, and every
+// warp of the grid takes an equal run of them, whatever sequences it spans.  A
+// warp streams its run through a ring of its own (one bulk copy for each tile,
+// which lies in one piece, lane 0 issuing), keeps a running maximum, sum and
+// accumulator in registers, and never waits for another warp until its run is
+// done.  Units (a sequence's KV head and row tile) that a run holds whole are
+// written out at once; what is left of a warp's run at its two ends is joined in
+// the CTA, and what is left of the CTA's run at its two ends by the join kernel,
+// always in the order of the tokens, so results repeat bit for bit.
+#pragma once
+
+#include <math_constants.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kv.cuh"
+
+namespace aq {
+namespace kv {
+
+namespace {
+
+__device__ uint32_t g_fault = 0;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kSms = 148;  // the grid never has more CTAs than these hold
+
+template <int BITS, int D, int G, int NT>
+struct Form {
+  static constexpr int kNG = D / G;                  // groups of a row
+  static constexpr int kRow = D * BITS / 8;          // bytes of a row of codes
+  static constexpr int kGroupBytes = G * BITS / 8;
+  static constexpr int kMeta = meta_bytes(D, G);     // bytes of a token's pairs
+  static constexpr int kTileBytes = tile_bytes(D, G, BITS);
+  // Tiles of a chunk: two share the maximum's shuffles; one where a ring of
+  // two-tile stages would leave no room for three stages.
+  static constexpr int kCT = kTileBytes > 4800 ? 1 : 2;
+  static constexpr int kStage = kCT * kTileBytes;
+  static constexpr int kRows = 8 * NT;               // query rows of a unit
+  static constexpr int kPart = kRows * (D + 2);      // floats of a partial result: max, sum, accumulator
+  // Two CTAs on an SM where their rings have two stages or more and 128 registers a thread hold the accumulator.
+  static constexpr int kSmem = 224 * 1024;
+  static constexpr int kCtas = (NT == 1 && D <= 128 && kSmem / 2 / (kWarps * kStage) >= 2) ? 2 : 1;
+  static constexpr int kStages = kSmem / kCtas / (kWarps * kStage) > 4 ? 4 : kSmem / kCtas / (kWarps * kStage);
+  static constexpr int kRing = kStages * kStage;     // bytes of a warp's ring
+  static_assert(kStages >= 2 && kRing >= kPart * 4, "a warp's ring holds two stages, and its last partial result");
+};
+
+// What a CTA leaves for the join: the unit that starts in its run and goes on
+// behind it (or -1), and the last CTA that has a part of it.
+struct Loose {
+  int unit, last;
+};
+
+struct Plan {
+  int ctas;          // of the launch
+  int row_tiles;     // of a KV head's query rows
+  float *parts;      // [ctas][2][kPart]: the unit that goes on from the CTA before, the one that goes on behind it
+  float *heads;      // [ctas][kWarps][kPart]: the end of a unit that another warp began
+  Loose *loose;      // [ctas]
+};
+
+// Positions that a sequence's new tokens see between them, as chunks.
+struct Span {
+  int len, first, chunks;  // first chunk; at least one, so that rows that see nothing are written too
+};
+template <int CHUNK>
+AQ_DEVICE Span span_of(const AttentionArgs &a, int seq) {
+  const int len32 = __ldg(a.c.lens + seq);
+  const int64_t len = len32, cap = int64_t(a.c.width) << a.c.page_shift;
+  const int64_t end = max(int64_t(0), min(len, cap));
+  const int64_t lo = a.window ? max(int64_t(0), min(end, len - a.tokens + 1 - a.window)) : 0;
+  const int first = static_cast<int>(lo / CHUNK);
+  return Span{len32, first, max(1, static_cast<int>((end + CHUNK - 1) / CHUNK) - first)};
+}
+
+AQ_DEVICE void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of 16-bit values held as mma fragments.
+AQ_DEVICE uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+AQ_DEVICE float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+AQ_DEVICE uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+AQ_DEVICE float2 pair_of(uint32_t sb) {  // (scale, bias)
+  return __half22float2(*reinterpret_cast<const __half2 *>(&sb));
+}
+
+// N words of shared memory in the widest loads that N words' alignment allows.
+template <int N>
+AQ_DEVICE void lds(uint32_t (&w)[N], const uint8_t *p) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    static_assert(N == 1, "1, 2 or a multiple of 4 words");
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
+}
+
+// A running state of one warp over one unit: NT column tiles of query rows.  A
+// lane holds the rows 8 nt + 2 (lane % 4) + {0, 1}.
+template <int BITS, int D, int G, int NT>
+struct State {
+  using F = Form<BITS, D, G, NT>;
+  uint32_t q[NT][D / 16][2];     // q's fragments: fp16, times the row's power of two
+  float qsum[NT][F::kNG][2];     // sum of q over each group, times 2^-24
+  float rs[NT][2];               // a raw score times this is a score in powers of 2
+  int hi[NT][2], lo[NT][2];      // positions [lo, hi) are seen
+  int hi_all, lo_all;            // [lo_all, hi_all): seen by every row
+  float m[NT][2], l[NT][2];      // reference (the maximum, see below) and sum of weights, the latter of this lane's tokens
+  float bias[NT][F::kNG][2];     // sum of weights times V biases, of this lane's tokens
+  float acc[NT][D / 16][4];      // sum of (weight * V scale) * code, times 2^-24
+  int e;                         // V scales so far are below 2^e
+};
+
+template <int BITS, int D, int G, int NT>
+AQ_DEVICE void start_unit(State<BITS, D, G, NT> &st, const AttentionArgs &a, int seq, int64_t len, int h, int row0) {
+  using F = Form<BITS, D, G, NT>;
+  constexpr int KW = F::kGroupBytes / 16;  // words of a lane in a group of K: a quarter
+  constexpr int PW = 32 / BITS;            // codes of a word
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rows = a.tokens * a.group;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = row0 + nt * 8 + g;
+    const bool real = r < rows;
+    const int j = real ? r / a.group : 0, i = real ? r - j * a.group : 0;
+    const uint16_t *q = a.q + seq * a.q_stride[0] + j * a.q_stride[1] + (h * a.group + i) * a.q_stride[2];
+    uint32_t raw[F::kNG][KW][PW / 2];
+    uint32_t top = 0;
+#pragma unroll
+    for (int gi = 0; gi < F::kNG; ++gi)
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const uint16_t *p = q + gi * G + (t * KW + w) * PW;
+        if constexpr (PW == 8) {
+          const uint4 v = real ? ldg_nc16(p) : make_uint4(0u, 0u, 0u, 0u);
+          raw[gi][w][0] = v.x, raw[gi][w][1] = v.y, raw[gi][w][2] = v.z, raw[gi][w][3] = v.w;
+        } else {
+          const uint2 v = real ? ldg_nc8(p) : make_uint2(0u, 0u);
+          raw[gi][w][0] = v.x, raw[gi][w][1] = v.y;
+        }
+#pragma unroll
+        for (int k = 0; k < PW / 2; ++k)
+          top = max(top, max(raw[gi][w][k] & 0x7FFFu, (raw[gi][w][k] >> 16) & 0x7FFFu));
+      }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // 2^e puts the row's largest |q| in [2^14, 2^15): bf16's 8 bits are exact in fp16 down to 2^-28 of it
+    const int e = min(120, max(-100, 141 - static_cast<int>(top >> 7)));
+    const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
+    float qsum[F::kNG];
+#pragma unroll
+    for (int gi = 0; gi < F::kNG; ++gi) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        float x[PW];
+#pragma unroll
+        for (int k = 0; k < PW / 2; ++k) {
+          x[2 * k] = __uint_as_float(raw[gi][w][k] << 16) * up;
+          x[2 * k + 1] = __uint_as_float(raw[gi][w][k] & 0xFFFF0000u) * up;
+        }
+        // the order in which unpack_k gives a word's codes
+        constexpr float up4 = BITS == 4 ? 0.0625f : 1.0f;
+#pragma unroll
+        for (int s = 0; s < PW / 4; ++s) {
+          const int k = (gi * KW + w) * (PW / 4) + s;
+          const int o = BITS == 4 ? 2 * s : 0, n = BITS == 4 ? 4 : 2;
+          st.q[nt][k][0] = pack_half2(x[o], x[o + n]);
+          st.q[nt][k][1] = pack_half2(x[o + 1] * up4, x[o + 1 + n] * up4);
+          const float2 f0 = pair_of(st.q[nt][k][0]), f1 = pair_of(st.q[nt][k][1]);
+          sum += f0.x + f0.y + (f1.x + f1.y) * (1.0f / up4);
+        }
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      qsum[gi] = sum * 0x1p-24f;
+    }
+    const float rs = ldexpf(fabsf(a.scale) * CUDART_L2E_F, 24 - e);
+    const int64_t cap = int64_t(a.c.width) << a.c.page_shift;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int src = (2 * t + c) * 4;
+#pragma unroll
+      for (int gi = 0; gi < F::kNG; ++gi) st.qsum[nt][gi][c] = __shfl_sync(0xffffffffu, qsum[gi], src);
+      st.rs[nt][c] = __shfl_sync(0xffffffffu, rs, src);
+      const int64_t p = len - a.tokens + min(row0 + nt * 8 + 2 * t + c, rows - 1) / a.group;  // the row's position
+      const int64_t hi = max(int64_t(0), min(p + 1, cap));
+      st.hi[nt][c] = static_cast<int>(hi);
+      st.lo[nt][c] = a.window ? static_cast<int>(max(int64_t(0), min(hi, p + 1 - a.window))) : 0;
+      st.m[nt][c] = -1e30f;
+      st.l[nt][c] = 0.0f;
+#pragma unroll
+      for (int gi = 0; gi < F::kNG; ++gi) st.bias[nt][gi][c] = 0.0f;
+    }
+#pragma unroll
+    for (int i2 = 0; i2 < D / 16; ++i2)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) st.acc[nt][i2][c] = 0.0f;
+    if (nt == 0) {
+      st.hi_all = __shfl_sync(0xffffffffu, st.hi[0][0], 0);
+    }
+    if (nt == NT - 1) {
+      st.lo_all = __shfl_sync(0xffffffffu, st.lo[nt][1], 3);
+    }
+  }
+  st.e = -14;
+}
+
+// The fp16 pairs of a word of K codes, in an order that q's fragments share.
+template <int BITS>
+AQ_DEVICE void unpack_k(uint32_t w, uint32_t (&x)[16 / BITS]) {
+  if constexpr (BITS == 4) {
+    x[0] = w & 0x000F000Fu;  // codes 0, 4
+    x[1] = w & 0x00F000F0u;  // codes 1, 5, times 16
+    x[2] = (w >> 8) & 0x000F000Fu;
+    x[3] = (w >> 8) & 0x00F000F0u;
+  } else {
+    x[0] = w & 0x00FF00FFu;  // codes 0, 2
+    x[1] = (w >> 8) & 0x00FF00FFu;
+  }
+}
+
+// One chunk: kCT tiles in shared memory, the first of them at position pos.
+// valid: bit i, tile i was copied.
+template <int BITS, int D, int G, int NT>
+AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int pos, uint32_t valid) {
+  using F = Form<BITS, D, G, NT>;
+  constexpr int KW = F::kGroupBytes / 16;
+  constexpr int CT = F::kCT, NG = F::kNG;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // The token of matrix row r (and 8 + r): such that the tokens that V's fragments want in lane t are t, t + 4, t + 8 and
+  // t + 12, neighbouring rows for neighbouring lanes.
+  const int tok = ((g & 1) << 2) | (g >> 1);
+  float x[CT][NT][4];
+  uint32_t sv[CT][2][NG];
+  const bool whole = valid == (1u << CT) - 1u && pos >= st.lo_all && pos + kTile * CT <= st.hi_all;
+  // --- scores
+#pragma unroll
+  for (int i = 0; i < CT; ++i) {
+    const uint8_t *tile = stage + i * F::kTileBytes;
+    const uint8_t *k0 = tile + tok * F::kRow + t * (KW * 4), *k1 = k0 + 8 * F::kRow;
+    const uint8_t *meta = tile + 2 * kTile * F::kRow + tok * F::kMeta;
+    uint32_t sk[2][NG];
+    lds<NG>(sk[0], meta);
+    lds<NG>(sk[1], meta + 8 * F::kMeta);
+    lds<NG>(sv[i][0], meta + F::kMeta / 2);
+    lds<NG>(sv[i][1], meta + 8 * F::kMeta + F::kMeta / 2);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[i][nt][c] = 0.0f;
+#pragma unroll
+    for (int gi = 0; gi < NG; ++gi) {
+      uint32_t w0[KW], w1[KW];
+      lds<KW>(w0, k0 + gi * F::kGroupBytes);
+      lds<KW>(w1, k1 + gi * F::kGroupBytes);
+      float s[NT][4] = {};
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        uint32_t a0[16 / BITS], a1[16 / BITS];
+        unpack_k<BITS>(w0[w], a0);
+        unpack_k<BITS>(w1[w], a1);
+#pragma unroll
+        for (int j = 0; j < 8 / BITS; ++j) {
+          const int k = (gi * KW + w) * (8 / BITS) + j;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(s[nt], a0[2 * j], a1[2 * j], a0[2 * j + 1], a1[2 * j + 1], st.q[nt][k][0], st.q[nt][k][1]);
+        }
+      }
+      const float2 p0 = pair_of(sk[0][gi]), p1 = pair_of(sk[1][gi]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          x[i][nt][c] = fmaf(p0.x, s[nt][c], fmaf(p0.y, st.qsum[nt][gi][c], x[i][nt][c]));
+          x[i][nt][2 + c] = fmaf(p1.x, s[nt][2 + c], fmaf(p1.y, st.qsum[nt][gi][c], x[i][nt][2 + c]));
+        }
+      }
+    }
+  }
+  // --- which tokens a row sees; what no row sees may be anything, so its scales and biases are not used
+  uint32_t seen = 0xFFFFFFFFu;  // bit (i * NT + nt) * 4 + c
+  if (!whole) {
+    seen = 0;
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int at = pos + i * kTile + half * 8 + tok;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const bool see = (valid >> i & 1) && at >= st.lo[nt][c] && at < st.hi[nt][c];
+            if (see) seen |= 1u << ((i * NT + nt) * 4 + half * 2 + c);
+            else x[i][nt][half * 2 + c] = -CUDART_INF_F;
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t mine = 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mine |= seen >> ((i * NT + nt) * 4 + half * 2) & 3u;
+        // the four lanes of a token hold different rows: what any of them sees counts
+        mine |= __shfl_xor_sync(0xffffffffu, mine, 1);
+        mine |= __shfl_xor_sync(0xffffffffu, mine, 2);
+        if (!mine) {
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi) sv[i][half][gi] = 0;
+        }
+      }
+    }
+  }
+  // --- the running reference.  A weight is 2^(x - m): m is the row's maximum so far + e - 15, where every V scale so far is
+  // below 2^e, so that (weight * scale) stays below 2^15 and is a normal fp16 down to 2^-29 of that: what rounds to nothing
+  // is smaller than a 2^-39th of the largest
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < CT; ++i)
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi) top = max(top, sv[i][half][gi] & 0x7FFFu);
+  const int e = max(st.e, static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 10) - 14);
+  float mx[NT][2];
+  bool more = e > st.e;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float v = fmaxf(x[0][nt][c], x[0][nt][2 + c]);
+#pragma unroll
+      for (int i = 1; i < CT; ++i) v = fmaxf(v, fmaxf(x[i][nt][c], x[i][nt][2 + c]));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+      mx[nt][c] = fmaf(v, st.rs[nt][c], static_cast<float>(e - 15));
+      more |= mx[nt][c] > st.m[nt][c];
+    }
+  if (__any_sync(0xffffffffu, more)) {
+    const float shift = static_cast<float>(e - st.e);
+    st.e = e;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float mn = fmaxf(st.m[nt][c] + shift, mx[nt][c]);
+        const float al = exp2_approx(st.m[nt][c] - mn);
+        st.m[nt][c] = mn;
+        st.l[nt][c] *= al;
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) st.bias[nt][gi][c] *= al;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          st.acc[nt][k][c] *= al;
+          st.acc[nt][k][2 + c] *= al;
+        }
+      }
+  }
+  // --- weights, and their products with V
+#pragma unroll
+  for (int i = 0; i < CT; ++i) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float p = exp2_approx(fmaf(x[i][nt][c], st.rs[nt][c & 1], -st.m[nt][c & 1]));
+        if (!whole && !(seen >> ((i * NT + nt) * 4 + c) & 1)) p = 0.0f;
+        x[i][nt][c] = p;
+        st.l[nt][c & 1] += p;
+      }
+    const uint8_t *v = stage + i * F::kTileBytes + kTile * F::kRow + t * F::kRow + g * (F::kGroupBytes / 8);
+#pragma unroll
+    for (int gi = 0; gi < NG; ++gi) {
+      const float2 p0 = pair_of(sv[i][0][gi]), p1 = pair_of(sv[i][1][gi]);
+      uint32_t b[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 sb = c < 2 ? p0 : p1;
+          y[c] = x[i][nt][c] * sb.x;
+          float z = x[i][nt][c] * sb.y;
+          // (a scale or bias that this row does not see may be infinite or NaN where another row's token is)
+          if (!whole && !(seen >> ((i * NT + nt) * 4 + c) & 1)) y[c] = z = 0.0f;
+          st.bias[nt][gi][c & 1] += z;
+        }
+        b[nt][0] = transpose8x8(pack_half2(y[0], y[1]));
+        b[nt][1] = transpose8x8(pack_half2(y[2], y[3]));
+      }
+      constexpr int VB = F::kGroupBytes / 8;        // bytes of a lane in a group of V: 2, 4, 8 or 16
+      constexpr int VW = VB < 4 ? 1 : VB / 4;
+      uint32_t w[4][VW];                            // tokens t, t + 4, t + 8, t + 12
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint8_t *p = v + 4 * k * F::kRow + gi * F::kGroupBytes;
+        if constexpr (VB < 4) w[k][0] = *reinterpret_cast<const uint16_t *>(p);
+        else lds<VW>(w[k], p);
+      }
+#pragma unroll
+      for (int j = 0; j < VW; ++j) {
+#pragma unroll
+        for (int half = 0; half < (VB < 4 ? 1 : 2); ++half) {
+          // 16 bits of codes of one token below those of another: pairs of one dimension
+          const uint32_t lo = __byte_perm(w[0][j], w[1][j], half ? 0x7632 : 0x5410);
+          const uint32_t hi = __byte_perm(w[2][j], w[3][j], half ? 0x7632 : 0x5410);
+          constexpr uint32_t M0 = BITS == 4 ? 0x000F000Fu : 0x00FF00FFu;
+          if constexpr (BITS == 4) {
+            const int mi = gi * (G / 16) + (j * 2 + half) * 2;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(st.acc[nt][mi], lo & M0, lo & 0x00F000F0u, hi & M0, hi & 0x00F000F0u, b[nt][0], b[nt][1]);
+              mma16816(st.acc[nt][mi + 1], (lo >> 8) & M0, (lo >> 8) & 0x00F000F0u, (hi >> 8) & M0,
+                       (hi >> 8) & 0x00F000F0u, b[nt][0], b[nt][1]);
+            }
+          } else {
+            const int mi = gi * (G / 16) + j * 2 + half;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(st.acc[nt][mi], lo & M0, (lo >> 8) & M0, hi & M0, (hi >> 8) & M0, b[nt][0], b[nt][1]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Sums over the lanes that share rows, then the accumulator in its true size: acc[nt][k][c] becomes the weighted sum of
+// dimension (k / (G / 16)) * G + g * (G / 8) + 2 (k % (G / 16)) + c / 2 for row 8 nt + 2 t + c % 2.
+template <int BITS, int D, int G, int NT>
+AQ_DEVICE void finish_unit(State<BITS, D, G, NT> &st) {
+  using F = Form<BITS, D, G, NT>;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        st.l[nt][c] += __shfl_xor_sync(0xffffffffu, st.l[nt][c], o);
+#pragma unroll
+        for (int gi = 0; gi < F::kNG; ++gi) st.bias[nt][gi][c] += __shfl_xor_sync(0xffffffffu, st.bias[nt][gi][c], o);
+      }
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const float b = st.bias[nt][k / (G / 16)][c];
+        st.acc[nt][k][c] = fmaf(st.acc[nt][k][c], 0x1p24f, b);
+        st.acc[nt][k][2 + c] = fmaf(st.acc[nt][k][2 + c], BITS == 4 ? 0x1p20f : 0x1p24f, b);
+      }
+    }
+}
+
+// Where row r of a unit goes: the flat row of out and lse.
+AQ_DEVICE int64_t out_row(const AttentionArgs &a, int seq, int h, int r) {
+  const int j = r / a.group, i = r - j * a.group;
+  return (int64_t(seq) * a.tokens + j) * a.q_heads + h * a.group + i;
+}
+
+AQ_DEVICE float log_sum(float m, float l) {
+  return l > 0.0f ? (m + __log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+}
+
+template <int BITS, int D, int G, int NT>
+AQ_DEVICE void write_out(const State<BITS, D, G, NT> &st, const AttentionArgs &a, int seq, int h, int row0) {
+  constexpr int VE = G / 8;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = row0 + nt * 8 + 2 * t + c;
+      if (r >= a.tokens * a.group) continue;
+      const int64_t row = out_row(a, seq, h, r);
+      const float inv = st.l[nt][c] > 0.0f ? 1.0f / st.l[nt][c] : st.l[nt][c];  // (0 stays 0, NaN stays NaN)
+#pragma unroll
+      for (int gi = 0; gi < D / G; ++gi) {
+        uint32_t u[VE / 2];
+#pragma unroll
+        for (int k = 0; k < VE / 2; ++k) {
+          const float *acc = st.acc[nt][gi * (G / 16) + k];
+          const __nv_bfloat162 p = __floats2bfloat162_rn(acc[c] * inv, acc[2 + c] * inv);
+          u[k] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+        uint16_t *dst = a.out + row * D + gi * G + g * VE;
+        if constexpr (VE == 4) {
+          *reinterpret_cast<uint2 *>(dst) = make_uint2(u[0], u[1]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < VE / 8; ++k)
+            reinterpret_cast<uint4 *>(dst)[k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+        }
+      }
+      if (a.lse && g == 0) a.lse[row] = log_sum(st.m[nt][c], st.l[nt][c]);
+    }
+}
+
+// A partial result: kRows references, kRows sums, then [kRows][D].
+template <int BITS, int D, int G, int NT>
+AQ_DEVICE void write_part(const State<BITS, D, G, NT> &st, float *part) {
+  using F = Form<BITS, D, G, NT>;
+  constexpr int VE = G / 8;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = nt * 8 + 2 * t + c;
+      if (g == 0) part[r] = st.m[nt][c], part[F::kRows + r] = st.l[nt][c];
+#pragma unroll
+      for (int gi = 0; gi < D / G; ++gi) {
+        float4 *dst = reinterpret_cast<float4 *>(part + 2 * F::kRows + r * D + gi * G + g * VE);
+#pragma unroll
+        for (int k = 0; k < VE / 4; ++k) {
+          const float *x = st.acc[nt][gi * (G / 16) + 2 * k], *y = st.acc[nt][gi * (G / 16) + 2 * k + 1];
+          dst[k] = make_float4(x[c], x[2 + c], y[c], y[2 + c]);
+        }
+      }
+    }
+}
+
+// Joins n partial results, part(0) .. part(n - 1) in this order: calls put(row, column / 4, sum, reference, weights' sum)
+// for every four columns.  All threads of the CTA.
+template <int ROWS, int D, class Part, class Put>
+AQ_DEVICE void join(int n, int threads, Part part, Put put) {
+  for (int i = threadIdx.x; i < ROWS * D / 4; i += threads) {
+    const int r = i / (D / 4), c = i - r * (D / 4);
+    float m = -1e30f;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[r]);
+    float l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float *p = part(k);
+      const float w = exp2_approx(p[r] - m);
+      const float4 v = reinterpret_cast<const float4 *>(p + 2 * ROWS)[i];
+      l = fmaf(w, p[ROWS + r], l);
+      o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    }
+    put(r, c, o, m, l);
+  }
+}
+
+// Writes four columns of row r of a unit to out, and the row's lse.
+template <int D>
+AQ_DEVICE void put_out(const AttentionArgs &a, int seq, int h, int r, int c, float4 o, float m, float l) {
+  if (r >= a.tokens * a.group) return;
+  const int64_t row = out_row(a, seq, h, r);
+  const float inv = l > 0.0f ? 1.0f / l : l;
+  const __nv_bfloat162 p = __floats2bfloat162_rn(o.x * inv, o.y * inv), q = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2 *>(a.out + row * D + c * 4) =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&q));
+  if (a.lse && c == 0) a.lse[row] = log_sum(m, l);
+}
+
+// A warp's place in the list of chunks: units are numbered sequence by sequence, heads and then row tiles within one.
+template <int CHUNK>
+struct Cursor {
+  int seq, unit;    // unit: of the sequence
+  int chunk;        // of the unit
+  Span span;
+  AQ_DEVICE void next_unit(const AttentionArgs &a, int units) {
+    chunk = 0;
+    if (++unit == units) {
+      unit = 0;
+      if (++seq < a.c.batch) span = span_of<CHUNK>(a, seq);
+    }
+  }
+};
+
+template <int BITS, int D, int G, int NT>
+__global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
+    attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Plan plan) {
+  using F = Form<BITS, D, G, NT>;
+  constexpr int CT = F::kCT, CHUNK = CT * kTile;
+  extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings
+  __shared__ uint64_t bars[kWarps][F::kStages];
+  __shared__ int sums[kThreads + 1], warp_sums[kWarps];
+  __shared__ int head_unit[kWarps], tail_unit[kWarps], tail_end[kWarps];
+  __shared__ bool tail_starts[kWarps];
+  __shared__ volatile int abort_flag;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+    for (int i = 0; i < F::kStages; ++i) mbar_init(&bars[warp][i], 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) abort_flag = 0;
+  // --- how many chunks there are, and where this warp's run begins: thread i counts its share of the sequences
+  const int units = a.c.heads * plan.row_tiles;  // of a sequence
+  const int per = (a.c.batch + kThreads - 1) / kThreads;
+  {
+    int n = 0;
+    for (int b = threadIdx.x * per; b < min(a.c.batch, (static_cast<int>(threadIdx.x) + 1) * per); ++b)
+      n += span_of<CHUNK>(a, b).chunks;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += warp_sums[w];
+    sums[threadIdx.x + 1] = before + incl;
+    if (threadIdx.x == 0) sums[0] = 0;
+    __syncthreads();
+  }
+  const int total = sums[kThreads] * units;
+  const int share = max(1, (total + plan.ctas * kWarps - 1) / (plan.ctas * kWarps));
+  const int begin = static_cast<int>(min(int64_t(total), (int64_t(blockIdx.x) * kWarps + warp) * share));
+  const int end = static_cast<int>(min(int64_t(total), int64_t(begin) + share));
+  if (lane == 0) head_unit[warp] = tail_unit[warp] = -1;
+  if (begin < end) {
+    Cursor<CHUNK> cur;
+    {
+      int lo = 0, hi = kThreads;  // the last share of sequences that begins at or before this run
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sums[mid] * units <= begin) lo = mid;
+        else hi = mid;
+      }
+      int at = sums[lo] * units;
+      cur.seq = lo * per;
+      cur.span = span_of<CHUNK>(a, cur.seq);
+      while (begin - at >= cur.span.chunks * units) {
+        at += cur.span.chunks * units;
+        cur.span = span_of<CHUNK>(a, ++cur.seq);
+      }
+      cur.unit = (begin - at) / cur.span.chunks;
+      cur.chunk = (begin - at) - cur.unit * cur.span.chunks;
+    }
+    uint8_t *ring = smem + warp * F::kRing;
+    // --- the copies: `ahead` runs kStages chunks in front of cur
+    Cursor<CHUNK> ahead = cur;
+    int issued = begin;
+    uint32_t valid_bits = 0;  // CT bits for each stage
+    // the table's entries of ahead's tiles are loaded one chunk early and looked at when their copies are issued
+    int page[CT];
+    uint32_t needed = 0;  // (only tiles that some row sees are looked up: entries in front of a window may hold anything)
+    auto look_up = [&]() {
+      const int64_t len = ahead.span.len, first = a.window ? len - a.tokens + 1 - a.window : 0;
+      needed = 0;
+#pragma unroll
+      for (int i = 0; i < CT; ++i) {
+        const int pos = (ahead.span.first + ahead.chunk) * CHUNK + i * kTile;
+        const int e = pos >> a.c.page_shift;
+        if (pos < len && pos + kTile > first && e < a.c.width) {
+          needed |= 1u << i;
+          page[i] = __ldg(a.c.table + int64_t(ahead.seq) * a.c.width + e);
+        }
+      }
+    };
+    auto issue = [&]() {
+      const int stage = (issued - begin) % F::kStages;
+      uint32_t ok = 0;
+#pragma unroll
+      for (int i = 0; i < CT; ++i)
+        ok |= ((needed >> i & 1) && static_cast<uint32_t>(page[i]) < static_cast<uint32_t>(a.c.pages) ? 1u : 0u) << i;
+      valid_bits = (valid_bits & ~(((1u << CT) - 1u) << (stage * CT))) | ok << (stage * CT);
+      if (lane == 0) {
+        uint64_t *bar = &bars[warp][stage];
+        mbar_arrive_expect_tx(bar, __popc(ok) * F::kTileBytes);
+        const int h = ahead.unit / plan.row_tiles;
+#pragma unroll
+        for (int i = 0; i < CT; ++i) {
+          if (ok >> i & 1) {
+            const int pos = (ahead.span.first + ahead.chunk) * CHUNK + i * kTile;
+            bulk_g2s(ring + stage * F::kStage + i * F::kTileBytes,
+                     a.c.data + tile_index(a.c, page[i], h, pos) * F::kTileBytes, F::kTileBytes, bar);
+          }
+        }
+        if (ok != needed) atomicOr(&g_fault, kFaultBadIndex);
+      }
+      if (++issued < end) {
+        if (++ahead.chunk == ahead.span.chunks) ahead.next_unit(a, units);
+        look_up();
+      }
+    };
+    look_up();
+    while (issued < end && issued - begin < F::kStages) issue();
+    // --- the run, unit by unit
+    bool ok = true;
+    int at = begin;
+    while (at < end && ok) {
+      const int h = cur.unit / plan.row_tiles, row0 = (cur.unit - h * plan.row_tiles) * F::kRows;
+      const int first = cur.chunk, take = min(cur.span.chunks - first, end - at);
+      State<BITS, D, G, NT> st;
+      start_unit(st, a, cur.seq, cur.span.len, h, row0);
+      for (int i = 0; i < take; ++i, ++at) {
+        const int n = at - begin, stage = n % F::kStages;
+        ok = mbar_wait(&bars[warp][stage], (n / F::kStages) & 1, &abort_flag, &g_fault, kFaultQmvWait);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        run_chunk(st, ring + stage * F::kStage, (cur.span.first + first + i) * CHUNK,
+                  valid_bits >> (stage * CT) & ((1u << CT) - 1u));
+        __syncwarp();
+        if (issued < end) issue();
+      }
+      if (!ok) break;
+      finish_unit(st);
+      const int id = cur.seq * units + cur.unit;
+      if (first == 0 && take == cur.span.chunks) {
+        write_out(st, a, cur.seq, h, row0);
+      } else if (first + take == cur.span.chunks) {
+        write_part(st, plan.heads + (int64_t(blockIdx.x) * kWarps + warp) * F::kPart);
+        if (lane == 0) head_unit[warp] = id;
+      } else {  // the warp's last: its ring is free
+        write_part(st, reinterpret_cast<float *>(ring));
+        if (lane == 0) {
+          tail_unit[warp] = id;
+          tail_end[warp] = at - first - take + cur.span.chunks;
+          tail_starts[warp] = first == 0;
+        }
+      }
+      if (cur.span.len > (int64_t(a.c.width) << a.c.page_shift) && lane == 0) atomicOr(&g_fault, kFaultBadIndex);
+      cur.next_unit(a, units);
+    }
+    if (!ok) {  // copies in flight land before the CTA goes
+      for (int n = at - begin; n < issued - begin; ++n) mbar_drain(&bars[warp][n % F::kStages], (n / F::kStages) & 1);
+    }
+  }
+  __syncthreads();
+  // --- what units have left at the warps' ends, in their order: the end of one that an earlier warp began (head), and the
+  // beginning or the middle of one that the next warp goes on with (tail)
+  Loose loose{-1, -1};
+  if (!abort_flag) {
+    int slot = 0;
+    while (slot < 2 * kWarps) {
+      auto unit_at = [&](int s) { return s & 1 ? tail_unit[s >> 1] : head_unit[s >> 1]; };
+      const int id = unit_at(slot);
+      if (id < 0) {
+        ++slot;
+        continue;
+      }
+      // a unit's parts lie in warps that follow one another, one in each
+      const int first = slot;
+      int last = slot, n = 0;
+      for (; slot < 2 * kWarps; ++slot) {
+        const int u = unit_at(slot);
+        if (u == id) last = slot, ++n;
+        else if (u >= 0) break;
+      }
+      const bool starts = (first & 1) && tail_starts[first >> 1], ends = !(last & 1);
+      auto part = [&](int k) -> const float * {
+        const int w = (first >> 1) + k;
+        return head_unit[w] == id ? plan.heads + (int64_t(blockIdx.x) * kWarps + w) * F::kPart
+                                  : reinterpret_cast<const float *>(smem + w * F::kRing);
+      };
+      const int seq = id / units, u = id - seq * units, h = u / plan.row_tiles, row0 = (u - h * plan.row_tiles) * F::kRows;
+      if (starts && ends) {
+        join<F::kRows, D>(n, kThreads, part, [&](int r, int c, float4 o, float m, float l) {
+          put_out<D>(a, seq, h, row0 + r, c, o, m, l);
+        });
+      } else {
+        float *dst = plan.parts + (int64_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * F::kPart;
+        join<F::kRows, D>(n, kThreads, part, [&](int r, int c, float4 o, float m, float l) {
+          if (c == 0) dst[r] = m, dst[F::kRows + r] = l;
+          reinterpret_cast<float4 *>(dst + 2 * F::kRows)[r * (D / 4) + c] = o;
+        });
+        if (starts) loose = Loose{id, (tail_end[first >> 1] - 1) / (kWarps * share)};
+      }
+    }
+  }
+  if (threadIdx.x == 0) plan.loose[blockIdx.x] = loose;
+}
+
+// Joins the units that several CTAs have a part of; CTA i takes the one that starts in CTA i's run and goes on behind it.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ AttentionArgs a,
+                                                        const __grid_constant__ Plan plan) {
+  constexpr int ROWS = 8 * NT, PART = ROWS * (D + 2);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Loose x = plan.loose[blockIdx.x];
+  if (x.unit < 0) return;
+  const int units = a.c.heads * plan.row_tiles;
+  const int seq = x.unit / units, u = x.unit - seq * units, h = u / plan.row_tiles;
+  const int row0 = (u - h * plan.row_tiles) * ROWS;
+  const int64_t cta = blockIdx.x;
+  join<ROWS, D>(
+      x.last - static_cast<int>(cta) + 1, kThreads,
+      [&](int k) -> const float * { return plan.parts + ((cta + k) * 2 + (k == 0 ? 1 : 0)) * PART; },
+      [&](int r, int c, float4 o, float m, float l) { put_out<D>(a, seq, h, row0 + r, c, o, m, l); });
+}
+
+struct Sizes {
+  int ctas, row_tiles;
+  size_t parts, heads, loose, bytes;  // offsets of the workspace's parts, and its size
+};
+
+template <int BITS, int D, int G, int NT>
+Sizes sizes_of(const AttentionArgs &a) {
+  using F = Form<BITS, D, G, NT>;
+  Sizes s;
+  s.row_tiles = (a.tokens * a.group + F::kRows - 1) / F::kRows;
+  // chunks that there can be; a CTA has one for each of its warps at least
+  int64_t most = ((int64_t(a.c.width) << a.c.page_shift) + F::kCT * kTile - 1) / (F::kCT * kTile) + 1;
+  if (a.window) most = std::min<int64_t>(most, (int64_t(a.window) + a.tokens) / (F::kCT * kTile) + 2);
+  const int64_t ctas = (int64_t(a.c.batch) * a.c.heads * s.row_tiles * most + kWarps - 1) / kWarps;
+  s.ctas = static_cast<int>(std::min<int64_t>(ctas, int64_t(kSms) * F::kCtas));
+  s.parts = 0;
+  s.heads = s.parts + size_t(s.ctas) * 2 * F::kPart * 4;
+  s.loose = s.heads + size_t(s.ctas) * kWarps * F::kPart * 4;
+  s.bytes = s.loose + size_t(s.ctas) * sizeof(Loose);
+  return s;
+}
+
+template <int BITS, int D, int G, int NT>
+cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
+  using F = Form<BITS, D, G, NT>;
+  auto kern = attention_kernel<BITS, D, G, NT>;
+  constexpr int kBytes = kWarps * F::kRing;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> ready{0};  // bit d: the attribute is set on device d
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  const Sizes s = sizes_of<BITS, D, G, NT>(a);
+  uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+  Plan plan;
+  plan.ctas = s.ctas;
+  plan.row_tiles = s.row_tiles;
+  plan.parts = reinterpret_cast<float *>(ws + s.parts);
+  plan.heads = reinterpret_cast<float *>(ws + s.heads);
+  plan.loose = reinterpret_cast<Loose *>(ws + s.loose);
+  kern<<<s.ctas, kThreads, kBytes, stream>>>(a, plan);
+  if ((e = cudaGetLastError()) != cudaSuccess || s.ctas == 1) return e;
+  // The join starts while the last CTAs run, and waits for them.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(s.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, a, plan);
+}
+
+// Calls run for a form: two column tiles of query rows where a KV head has more than eight rows and
+// the accumulators of both fit a thread's registers.
+template <class Run>
+auto by_form(const AttentionArgs &a, int D, int G, Run run) {
+  const bool two = a.tokens * int64_t(a.group) > 8;
+  if (D == 64) {
+    if (G == 32) return two ? run(Int<64>{}, Int<32>{}, Int<2>{}) : run(Int<64>{}, Int<32>{}, Int<1>{});
+    return two ? run(Int<64>{}, Int<64>{}, Int<2>{}) : run(Int<64>{}, Int<64>{}, Int<1>{});
+  }
+  if (D == 128) {
+    if (G == 32) return two ? run(Int<128>{}, Int<32>{}, Int<2>{}) : run(Int<128>{}, Int<32>{}, Int<1>{});
+    if (G == 64) return two ? run(Int<128>{}, Int<64>{}, Int<2>{}) : run(Int<128>{}, Int<64>{}, Int<1>{});
+    return two ? run(Int<128>{}, Int<128>{}, Int<2>{}) : run(Int<128>{}, Int<128>{}, Int<1>{});
+  }
+  if (G == 32) return run(Int<256>{}, Int<32>{}, Int<1>{});
+  if (G == 64) return run(Int<256>{}, Int<64>{}, Int<1>{});
+  return run(Int<256>{}, Int<128>{}, Int<1>{});
+}
+
+template <int BITS>
+cudaError_t launch_bits(const AttentionArgs &a, int D, int G, cudaStream_t s) {
+  return by_form(a, D, G, [&](auto d, auto g, auto nt) {
+    return launch_form<BITS, decltype(d)::value, decltype(g)::value, decltype(nt)::value>(a, s);
+  });
+}
+
+template <int BITS>
+size_t workspace_bits(const AttentionArgs &a, int D, int G) {
+  return by_form(a, D, G, [&](auto d, auto g, auto nt) {
+    return sizes_of<BITS, decltype(d)::value, decltype(g)::value, decltype(nt)::value>(a).bytes;
+  });
+}
+
+cudaError_t read_and_clear_fault_bits(uint32_t *word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_fault, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  const uint32_t zero = 0;
+  return cudaMemcpyToSymbol(g_fault, &zero, sizeof(uint32_t));
+}
+
+}  // namespace
+}  // namespace kv
+}  // namespace aq
