@@ -103,6 +103,13 @@ AQ_DEVICE void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, ui
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with a zero in place of the accumulator.
+AQ_DEVICE void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 // The transpose of an 8 x 8 matrix of 16-bit values held as mma fragments.
 AQ_DEVICE uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
@@ -156,37 +163,69 @@ struct State {
   int e;                         // V scales so far are below 2^e
 };
 
+// The query rows of a unit, as this lane's share of them: loaded early, looked at by start_unit.
 template <int BITS, int D, int G, int NT>
-AQ_DEVICE void start_unit(State<BITS, D, G, NT> &st, const AttentionArgs &a, int seq, int64_t len, int h, int row0) {
-  using F = Form<BITS, D, G, NT>;
-  constexpr int KW = F::kGroupBytes / 16;  // words of a lane in a group of K: a quarter
-  constexpr int PW = 32 / BITS;            // codes of a word
+struct Queries {
+  static constexpr int kKW = G * BITS / 128;  // words of a lane in a group of K: a quarter
+  static constexpr int kPW = 32 / BITS;       // codes of a word
+  uint32_t raw[NT][D / G][kKW][kPW / 2];
+};
+
+template <int BITS, int D, int G, int NT>
+AQ_DEVICE void load_queries(Queries<BITS, D, G, NT> &x, const AttentionArgs &a, int seq, int h, int row0) {
+  using Q = Queries<BITS, D, G, NT>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rows = a.tokens * a.group;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = row0 + nt * 8 + g;
-    const bool real = r < rows;
-    const int j = real ? r / a.group : 0, i = real ? r - j * a.group : 0;
+    const bool real = r < a.tokens * a.group;
+    const int j = a.tokens == 1 || !real ? 0 : r / a.group, i = real ? r - j * a.group : 0;
     const uint16_t *q = a.q + seq * a.q_stride[0] + j * a.q_stride[1] + (h * a.group + i) * a.q_stride[2];
-    uint32_t raw[F::kNG][KW][PW / 2];
+#pragma unroll
+    for (int gi = 0; gi < D / G; ++gi)
+#pragma unroll
+      for (int w = 0; w < Q::kKW; ++w) {
+        const uint16_t *p = q + gi * G + (t * Q::kKW + w) * Q::kPW;
+        uint32_t(&v)[Q::kPW / 2] = x.raw[nt][gi][w];
+        if constexpr (Q::kPW == 8) {
+          const uint4 u = real ? ldg_nc16(p) : make_uint4(0u, 0u, 0u, 0u);
+          v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+        } else {
+          const uint2 u = real ? ldg_nc8(p) : make_uint2(0u, 0u);
+          v[0] = u.x, v[1] = u.y;
+        }
+      }
+  }
+}
+
+template <int BITS, int D, int G, int NT>
+AQ_DEVICE void start_unit(State<BITS, D, G, NT> &st, const Queries<BITS, D, G, NT> &in, const AttentionArgs &a,
+                          int64_t len, int row0) {
+  using F = Form<BITS, D, G, NT>;
+  using Q = Queries<BITS, D, G, NT>;
+  constexpr int KW = Q::kKW, PW = Q::kPW;
+  const int t = threadIdx.x & 3;
+  const int64_t cap = int64_t(a.c.width) << a.c.page_shift;
+  // the positions that the unit's first and last rows, and with them all of its rows, stand at
+  auto position = [&](int r) { return len - a.tokens + (a.tokens == 1 ? 0 : min(r, a.tokens * a.group - 1) / a.group); };
+  auto end_of = [&](int64_t p) { return static_cast<int>(max(int64_t(0), min(p + 1, cap))); };
+  auto begin_of = [&](int64_t p) {
+    return a.window ? static_cast<int>(max(int64_t(0), min(int64_t(end_of(p)), p + 1 - a.window))) : 0;
+  };
+  st.hi_all = end_of(position(row0));
+  st.lo_all = begin_of(position(row0 + F::kRows - 1));
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
     uint32_t top = 0;
 #pragma unroll
     for (int gi = 0; gi < F::kNG; ++gi)
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const uint16_t *p = q + gi * G + (t * KW + w) * PW;
-        if constexpr (PW == 8) {
-          const uint4 v = real ? ldg_nc16(p) : make_uint4(0u, 0u, 0u, 0u);
-          raw[gi][w][0] = v.x, raw[gi][w][1] = v.y, raw[gi][w][2] = v.z, raw[gi][w][3] = v.w;
-        } else {
-          const uint2 v = real ? ldg_nc8(p) : make_uint2(0u, 0u);
-          raw[gi][w][0] = v.x, raw[gi][w][1] = v.y;
-        }
+      for (int w = 0; w < KW; ++w)
 #pragma unroll
-        for (int k = 0; k < PW / 2; ++k)
-          top = max(top, max(raw[gi][w][k] & 0x7FFFu, (raw[gi][w][k] >> 16) & 0x7FFFu));
-      }
+        for (int k = 0; k < PW / 2; ++k) {
+          const uint32_t v = in.raw[nt][gi][w][k];
+          top = max(top, max(v & 0x7FFFu, (v >> 16) & 0x7FFFu));
+        }
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     // 2^e puts the row's largest |q| in [2^14, 2^15): bf16's 8 bits are exact in fp16 down to 2^-28 of it
@@ -201,8 +240,8 @@ AQ_DEVICE void start_unit(State<BITS, D, G, NT> &st, const AttentionArgs &a, int
         float x[PW];
 #pragma unroll
         for (int k = 0; k < PW / 2; ++k) {
-          x[2 * k] = __uint_as_float(raw[gi][w][k] << 16) * up;
-          x[2 * k + 1] = __uint_as_float(raw[gi][w][k] & 0xFFFF0000u) * up;
+          x[2 * k] = __uint_as_float(in.raw[nt][gi][w][k] << 16) * up;
+          x[2 * k + 1] = __uint_as_float(in.raw[nt][gi][w][k] & 0xFFFF0000u) * up;
         }
         // the order in which unpack_k gives a word's codes
         constexpr float up4 = BITS == 4 ? 0.0625f : 1.0f;
@@ -221,32 +260,24 @@ AQ_DEVICE void start_unit(State<BITS, D, G, NT> &st, const AttentionArgs &a, int
       qsum[gi] = sum * 0x1p-24f;
     }
     const float rs = ldexpf(fabsf(a.scale) * CUDART_L2E_F, 24 - e);
-    const int64_t cap = int64_t(a.c.width) << a.c.page_shift;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int src = (2 * t + c) * 4;
 #pragma unroll
       for (int gi = 0; gi < F::kNG; ++gi) st.qsum[nt][gi][c] = __shfl_sync(0xffffffffu, qsum[gi], src);
       st.rs[nt][c] = __shfl_sync(0xffffffffu, rs, src);
-      const int64_t p = len - a.tokens + min(row0 + nt * 8 + 2 * t + c, rows - 1) / a.group;  // the row's position
-      const int64_t hi = max(int64_t(0), min(p + 1, cap));
-      st.hi[nt][c] = static_cast<int>(hi);
-      st.lo[nt][c] = a.window ? static_cast<int>(max(int64_t(0), min(hi, p + 1 - a.window))) : 0;
+      const int64_t p = position(row0 + nt * 8 + 2 * t + c);
+      st.hi[nt][c] = end_of(p);
+      st.lo[nt][c] = begin_of(p);
       st.m[nt][c] = -1e30f;
       st.l[nt][c] = 0.0f;
 #pragma unroll
       for (int gi = 0; gi < F::kNG; ++gi) st.bias[nt][gi][c] = 0.0f;
     }
 #pragma unroll
-    for (int i2 = 0; i2 < D / 16; ++i2)
+    for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) st.acc[nt][i2][c] = 0.0f;
-    if (nt == 0) {
-      st.hi_all = __shfl_sync(0xffffffffu, st.hi[0][0], 0);
-    }
-    if (nt == NT - 1) {
-      st.lo_all = __shfl_sync(0xffffffffu, st.lo[nt][1], 3);
-    }
+      for (int c = 0; c < 4; ++c) st.acc[nt][k][c] = 0.0f;
   }
   st.e = -14;
 }
@@ -266,8 +297,8 @@ AQ_DEVICE void unpack_k(uint32_t w, uint32_t (&x)[16 / BITS]) {
 }
 
 // One chunk: kCT tiles in shared memory, the first of them at position pos.
-// valid: bit i, tile i was copied.
-template <int BITS, int D, int G, int NT>
+// valid: bit i, tile i was copied.  WHOLE: every row sees every token.
+template <bool WHOLE, int BITS, int D, int G, int NT>
 AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int pos, uint32_t valid) {
   using F = Form<BITS, D, G, NT>;
   constexpr int KW = F::kGroupBytes / 16;
@@ -278,7 +309,6 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
   const int tok = ((g & 1) << 2) | (g >> 1);
   float x[CT][NT][4];
   uint32_t sv[CT][2][NG];
-  const bool whole = valid == (1u << CT) - 1u && pos >= st.lo_all && pos + kTile * CT <= st.hi_all;
   // --- scores
 #pragma unroll
   for (int i = 0; i < CT; ++i) {
@@ -299,7 +329,7 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
       uint32_t w0[KW], w1[KW];
       lds<KW>(w0, k0 + gi * F::kGroupBytes);
       lds<KW>(w1, k1 + gi * F::kGroupBytes);
-      float s[NT][4] = {};
+      float s[NT][4];
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
         uint32_t a0[16 / BITS], a1[16 / BITS];
@@ -309,8 +339,12 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
         for (int j = 0; j < 8 / BITS; ++j) {
           const int k = (gi * KW + w) * (8 / BITS) + j;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(s[nt], a0[2 * j], a1[2 * j], a0[2 * j + 1], a1[2 * j + 1], st.q[nt][k][0], st.q[nt][k][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if (w == 0 && j == 0)
+              mma16816_first(s[nt], a0[0], a1[0], a0[1], a1[1], st.q[nt][k][0], st.q[nt][k][1]);
+            else
+              mma16816(s[nt], a0[2 * j], a1[2 * j], a0[2 * j + 1], a1[2 * j + 1], st.q[nt][k][0], st.q[nt][k][1]);
+          }
         }
       }
       const float2 p0 = pair_of(sk[0][gi]), p1 = pair_of(sk[1][gi]);
@@ -326,7 +360,7 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
   }
   // --- which tokens a row sees; what no row sees may be anything, so its scales and biases are not used
   uint32_t seen = 0xFFFFFFFFu;  // bit (i * NT + nt) * 4 + c
-  if (!whole) {
+  if constexpr (!WHOLE) {
     seen = 0;
 #pragma unroll
     for (int i = 0; i < CT; ++i) {
@@ -414,7 +448,7 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         float p = exp2_approx(fmaf(x[i][nt][c], st.rs[nt][c & 1], -st.m[nt][c & 1]));
-        if (!whole && !(seen >> ((i * NT + nt) * 4 + c) & 1)) p = 0.0f;
+        if (!WHOLE && !(seen >> ((i * NT + nt) * 4 + c) & 1)) p = 0.0f;
         x[i][nt][c] = p;
         st.l[nt][c & 1] += p;
       }
@@ -432,7 +466,7 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
           y[c] = x[i][nt][c] * sb.x;
           float z = x[i][nt][c] * sb.y;
           // (a scale or bias that this row does not see may be infinite or NaN where another row's token is)
-          if (!whole && !(seen >> ((i * NT + nt) * 4 + c) & 1)) y[c] = z = 0.0f;
+          if (!WHOLE && !(seen >> ((i * NT + nt) * 4 + c) & 1)) y[c] = z = 0.0f;
           st.bias[nt][gi][c & 1] += z;
         }
         b[nt][0] = transpose8x8(pack_half2(y[0], y[1]));
@@ -567,24 +601,27 @@ AQ_DEVICE void write_part(const State<BITS, D, G, NT> &st, float *part) {
     }
 }
 
-// Joins n partial results, part(0) .. part(n - 1) in this order: calls put(row, column / 4, sum, reference, weights' sum)
-// for every four columns.  All threads of the CTA.
-template <int ROWS, int D, class Part, class Put>
-AQ_DEVICE void join(int n, int threads, Part part, Put put) {
-  for (int i = threadIdx.x; i < ROWS * D / 4; i += threads) {
+// Joins n <= MAX partial results, part(0) .. part(n - 1) in this order: calls put(row, column / 4, sum, reference,
+// weights' sum) for every four columns.  All threads of the CTA.
+template <int ROWS, int D, int MAX, class Part, class Put>
+AQ_DEVICE void join(int n, Part part, Put put) {
+  for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
     const int r = i / (D / 4), c = i - r * (D / 4);
-    float m = -1e30f;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[r]);
-    float l = 0.0f;
+    float mk[MAX], m = -1e30f, l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < MAX; ++k) mk[k] = k < n ? part(k)[r] : -1e30f;
+#pragma unroll
+    for (int k = 0; k < MAX; ++k) m = fmaxf(m, mk[k]);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float *p = part(k);
-      const float w = exp2_approx(p[r] - m);
-      const float4 v = reinterpret_cast<const float4 *>(p + 2 * ROWS)[i];
-      l = fmaf(w, p[ROWS + r], l);
-      o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+#pragma unroll
+    for (int k = 0; k < MAX; ++k) {
+      if (k < n) {
+        const float *p = part(k);
+        const float w = exp2_approx(mk[k] - m);
+        const float4 v = reinterpret_cast<const float4 *>(p + 2 * ROWS)[i];
+        l = fmaf(w, p[ROWS + r], l);
+        o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+      }
     }
     put(r, c, o, m, l);
   }
@@ -605,15 +642,16 @@ AQ_DEVICE void put_out(const AttentionArgs &a, int seq, int h, int r, int c, flo
 // A warp's place in the list of chunks: units are numbered sequence by sequence, heads and then row tiles within one.
 template <int CHUNK>
 struct Cursor {
-  int seq, unit;    // unit: of the sequence
-  int chunk;        // of the unit
+  int seq, head, row_tile;
+  int chunk;  // of the unit
   Span span;
-  AQ_DEVICE void next_unit(const AttentionArgs &a, int units) {
+  AQ_DEVICE void next_unit(const AttentionArgs &a, int row_tiles) {
     chunk = 0;
-    if (++unit == units) {
-      unit = 0;
-      if (++seq < a.c.batch) span = span_of<CHUNK>(a, seq);
-    }
+    if (++row_tile < row_tiles) return;
+    row_tile = 0;
+    if (++head < a.c.heads) return;
+    head = 0;
+    if (++seq < a.c.batch) span = span_of<CHUNK>(a, seq);
   }
 };
 
@@ -677,81 +715,79 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
         at += cur.span.chunks * units;
         cur.span = span_of<CHUNK>(a, ++cur.seq);
       }
-      cur.unit = (begin - at) / cur.span.chunks;
-      cur.chunk = (begin - at) - cur.unit * cur.span.chunks;
+      const int unit = (begin - at) / cur.span.chunks;
+      cur.chunk = (begin - at) - unit * cur.span.chunks;
+      cur.head = unit / plan.row_tiles;
+      cur.row_tile = unit - cur.head * plan.row_tiles;
     }
     uint8_t *ring = smem + warp * F::kRing;
-    // --- the copies: `ahead` runs kStages chunks in front of cur
+    // --- the copies: `ahead` runs kStages chunks in front of cur.  Lane i < CT looks after a chunk's tile i: it loads the
+    // table's entry one chunk early and looks at it when the copies are issued
     Cursor<CHUNK> ahead = cur;
-    int issued = begin;
-    uint32_t valid_bits = 0;  // CT bits for each stage
-    // the table's entries of ahead's tiles are loaded one chunk early and looked at when their copies are issued
-    int page[CT];
-    uint32_t needed = 0;  // (only tiles that some row sees are looked up: entries in front of a window may hold anything)
+    int left = end - begin, flying = 0, stage_in = 0;  // chunks not yet issued, and issued but not yet used
+    uint32_t valid_bits = 0;               // CT bits for each stage
+    int page = 0;
+    bool needed = false;
     auto look_up = [&]() {
-      const int64_t len = ahead.span.len, first = a.window ? len - a.tokens + 1 - a.window : 0;
-      needed = 0;
-#pragma unroll
-      for (int i = 0; i < CT; ++i) {
-        const int pos = (ahead.span.first + ahead.chunk) * CHUNK + i * kTile;
-        const int e = pos >> a.c.page_shift;
-        if (pos < len && pos + kTile > first && e < a.c.width) {
-          needed |= 1u << i;
-          page[i] = __ldg(a.c.table + int64_t(ahead.seq) * a.c.width + e);
-        }
-      }
+      // (only tiles that some row sees: entries in front of a window may hold anything)
+      const int pos = (ahead.span.first + ahead.chunk) * CHUNK + lane * kTile, e = pos >> a.c.page_shift;
+      needed = lane < CT && pos < ahead.span.len && e < a.c.width &&
+               (a.window == 0 || pos + kTile > int64_t(ahead.span.len) - a.tokens + 1 - a.window);
+      if (needed) page = __ldg(a.c.table + int64_t(ahead.seq) * a.c.width + e);
     };
     auto issue = [&]() {
-      const int stage = (issued - begin) % F::kStages;
-      uint32_t ok = 0;
-#pragma unroll
-      for (int i = 0; i < CT; ++i)
-        ok |= ((needed >> i & 1) && static_cast<uint32_t>(page[i]) < static_cast<uint32_t>(a.c.pages) ? 1u : 0u) << i;
-      valid_bits = (valid_bits & ~(((1u << CT) - 1u) << (stage * CT))) | ok << (stage * CT);
-      if (lane == 0) {
-        uint64_t *bar = &bars[warp][stage];
-        mbar_arrive_expect_tx(bar, __popc(ok) * F::kTileBytes);
-        const int h = ahead.unit / plan.row_tiles;
-#pragma unroll
-        for (int i = 0; i < CT; ++i) {
-          if (ok >> i & 1) {
-            const int pos = (ahead.span.first + ahead.chunk) * CHUNK + i * kTile;
-            bulk_g2s(ring + stage * F::kStage + i * F::kTileBytes,
-                     a.c.data + tile_index(a.c, page[i], h, pos) * F::kTileBytes, F::kTileBytes, bar);
-          }
-        }
-        if (ok != needed) atomicOr(&g_fault, kFaultBadIndex);
+      const bool there = needed && static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.pages);
+      const uint32_t ok = __ballot_sync(0xffffffffu, there);
+      valid_bits = (valid_bits & ~(((1u << CT) - 1u) << (stage_in * CT))) | ok << (stage_in * CT);
+      uint64_t *bar = &bars[warp][stage_in];
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(ok) * F::kTileBytes);
+      __syncwarp();
+      if (there) {
+        const int pos = (ahead.span.first + ahead.chunk) * CHUNK + lane * kTile;
+        bulk_g2s(ring + stage_in * F::kStage + lane * F::kTileBytes,
+                 a.c.data + tile_index(a.c, page, ahead.head, pos) * F::kTileBytes, F::kTileBytes, bar);
+      } else if (needed) {
+        atomicOr(&g_fault, kFaultBadIndex);
       }
-      if (++issued < end) {
-        if (++ahead.chunk == ahead.span.chunks) ahead.next_unit(a, units);
+      if (++stage_in == F::kStages) stage_in = 0;
+      ++flying;
+      if (--left > 0) {
+        if (++ahead.chunk == ahead.span.chunks) ahead.next_unit(a, plan.row_tiles);
         look_up();
       }
     };
     look_up();
-    while (issued < end && issued - begin < F::kStages) issue();
+    Queries<BITS, D, G, NT> queries;
+    load_queries(queries, a, cur.seq, cur.head, cur.row_tile * F::kRows);
+    for (int i = 0; i < F::kStages && left > 0; ++i) issue();
     // --- the run, unit by unit
     bool ok = true;
-    int at = begin;
-    while (at < end && ok) {
-      const int h = cur.unit / plan.row_tiles, row0 = (cur.unit - h * plan.row_tiles) * F::kRows;
+    int at = begin, stage = 0, parity = 0;
+    while (true) {
+      const int row0 = cur.row_tile * F::kRows;
       const int first = cur.chunk, take = min(cur.span.chunks - first, end - at);
       State<BITS, D, G, NT> st;
-      start_unit(st, a, cur.seq, cur.span.len, h, row0);
-      for (int i = 0; i < take; ++i, ++at) {
-        const int n = at - begin, stage = n % F::kStages;
-        ok = mbar_wait(&bars[warp][stage], (n / F::kStages) & 1, &abort_flag, &g_fault, kFaultQmvWait);
+      start_unit(st, queries, a, cur.span.len, row0);
+      int pos = (cur.span.first + first) * CHUNK;
+      for (int i = 0; i < take; ++i, pos += CHUNK) {
+        ok = mbar_wait(&bars[warp][stage], parity, &abort_flag, &g_fault, kFaultQmvWait);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        run_chunk(st, ring + stage * F::kStage, (cur.span.first + first + i) * CHUNK,
-                  valid_bits >> (stage * CT) & ((1u << CT) - 1u));
+        --flying;
+        const uint8_t *tiles = ring + stage * F::kStage;
+        const uint32_t valid = valid_bits >> (stage * CT) & ((1u << CT) - 1u);
+        if (valid == (1u << CT) - 1u && pos >= st.lo_all && pos + CHUNK <= st.hi_all) run_chunk<true>(st, tiles, pos, valid);
+        else run_chunk<false>(st, tiles, pos, valid);
         __syncwarp();
-        if (issued < end) issue();
+        if (left > 0) issue();
+        if (++stage == F::kStages) stage = 0, parity ^= 1;
       }
       if (!ok) break;
+      at += take;
       finish_unit(st);
-      const int id = cur.seq * units + cur.unit;
+      const int id = cur.seq * units + cur.head * plan.row_tiles + cur.row_tile;
       if (first == 0 && take == cur.span.chunks) {
-        write_out(st, a, cur.seq, h, row0);
+        write_out(st, a, cur.seq, cur.head, row0);
       } else if (first + take == cur.span.chunks) {
         write_part(st, plan.heads + (int64_t(blockIdx.x) * kWarps + warp) * F::kPart);
         if (lane == 0) head_unit[warp] = id;
@@ -764,10 +800,15 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
         }
       }
       if (cur.span.len > (int64_t(a.c.width) << a.c.page_shift) && lane == 0) atomicOr(&g_fault, kFaultBadIndex);
-      cur.next_unit(a, units);
+      if (at >= end) break;
+      cur.next_unit(a, plan.row_tiles);
+      load_queries(queries, a, cur.seq, cur.head, cur.row_tile * F::kRows);
     }
     if (!ok) {  // copies in flight land before the CTA goes
-      for (int n = at - begin; n < issued - begin; ++n) mbar_drain(&bars[warp][n % F::kStages], (n / F::kStages) & 1);
+      for (; flying > 0; --flying) {
+        mbar_drain(&bars[warp][stage], parity);
+        if (++stage == F::kStages) stage = 0, parity ^= 1;
+      }
     }
   }
   __syncthreads();
@@ -775,36 +816,31 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
   // beginning or the middle of one that the next warp goes on with (tail)
   Loose loose{-1, -1};
   if (!abort_flag) {
-    int slot = 0;
-    while (slot < 2 * kWarps) {
-      auto unit_at = [&](int s) { return s & 1 ? tail_unit[s >> 1] : head_unit[s >> 1]; };
-      const int id = unit_at(slot);
-      if (id < 0) {
-        ++slot;
-        continue;
-      }
-      // a unit's parts lie in warps that follow one another, one in each
-      const int first = slot;
-      int last = slot, n = 0;
-      for (; slot < 2 * kWarps; ++slot) {
-        const int u = unit_at(slot);
-        if (u == id) last = slot, ++n;
-        else if (u >= 0) break;
-      }
+    // slot 2 w: warp w's head, slot 2 w + 1: its tail; lane s looks at slot s
+    const int slot = lane & 15, mine = slot & 1 ? tail_unit[slot >> 1] : head_unit[slot >> 1];
+    const uint32_t used = __ballot_sync(0xffffffffu, mine >= 0) & 0xFFFFu, below = used & ((1u << slot) - 1u);
+    const int before = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
+    uint32_t firsts = __ballot_sync(0xffffffffu, mine >= 0 && (!below || before != mine)) & 0xFFFFu;
+    while (firsts) {
+      // a unit's parts lie in warps that follow one another, one in each; only the last of them can be a head
+      const int first = __ffs(firsts) - 1;
+      firsts &= firsts - 1;
+      const uint32_t members = used & ((firsts ? firsts & -firsts : 0x10000u) - (1u << first));
+      const int n = __popc(members), last = 31 - __clz(members), id = __shfl_sync(0xffffffffu, mine, first);
       const bool starts = (first & 1) && tail_starts[first >> 1], ends = !(last & 1);
+      const float *end_part = plan.heads + (int64_t(blockIdx.x) * kWarps + (last >> 1)) * F::kPart;
       auto part = [&](int k) -> const float * {
-        const int w = (first >> 1) + k;
-        return head_unit[w] == id ? plan.heads + (int64_t(blockIdx.x) * kWarps + w) * F::kPart
-                                  : reinterpret_cast<const float *>(smem + w * F::kRing);
+        return ends && k == n - 1 ? end_part : reinterpret_cast<const float *>(smem + ((first >> 1) + k) * F::kRing);
       };
-      const int seq = id / units, u = id - seq * units, h = u / plan.row_tiles, row0 = (u - h * plan.row_tiles) * F::kRows;
       if (starts && ends) {
-        join<F::kRows, D>(n, kThreads, part, [&](int r, int c, float4 o, float m, float l) {
+        const int seq = id / units, u = id - seq * units, h = u / plan.row_tiles;
+        const int row0 = (u - h * plan.row_tiles) * F::kRows;
+        join<F::kRows, D, kWarps>(n, part, [&](int r, int c, float4 o, float m, float l) {
           put_out<D>(a, seq, h, row0 + r, c, o, m, l);
         });
       } else {
         float *dst = plan.parts + (int64_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * F::kPart;
-        join<F::kRows, D>(n, kThreads, part, [&](int r, int c, float4 o, float m, float l) {
+        join<F::kRows, D, kWarps>(n, part, [&](int r, int c, float4 o, float m, float l) {
           if (c == 0) dst[r] = m, dst[F::kRows + r] = l;
           reinterpret_cast<float4 *>(dst + 2 * F::kRows)[r * (D / 4) + c] = o;
         });
@@ -815,22 +851,72 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
   if (threadIdx.x == 0) plan.loose[blockIdx.x] = loose;
 }
 
-// Joins the units that several CTAs have a part of; CTA i takes the one that starts in CTA i's run and goes on behind it.
+// Joins the units that several CTAs have a part of: block (i, r) takes row r of the one that starts in CTA i's run and
+// goes on behind it.  Threads share the parts (there are up to as many as CTAs) as well as the columns.
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ AttentionArgs a,
                                                         const __grid_constant__ Plan plan) {
-  constexpr int ROWS = 8 * NT, PART = ROWS * (D + 2);
+  constexpr int ROWS = 8 * NT, PART = ROWS * (D + 2), COLS = D / 4, SHARES = kThreads / COLS, MOST = 2 * kSms;
+  __shared__ float weights[MOST], red[2][kWarps];
+  __shared__ float4 sums[SHARES][COLS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = blockIdx.y, cta = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Loose x = plan.loose[blockIdx.x];
+  const Loose x = plan.loose[cta];
   if (x.unit < 0) return;
   const int units = a.c.heads * plan.row_tiles;
   const int seq = x.unit / units, u = x.unit - seq * units, h = u / plan.row_tiles;
-  const int row0 = (u - h * plan.row_tiles) * ROWS;
-  const int64_t cta = blockIdx.x;
-  join<ROWS, D>(
-      x.last - static_cast<int>(cta) + 1, kThreads,
-      [&](int k) -> const float * { return plan.parts + ((cta + k) * 2 + (k == 0 ? 1 : 0)) * PART; },
-      [&](int r, int c, float4 o, float m, float l) { put_out<D>(a, seq, h, row0 + r, c, o, m, l); });
+  const int row = (u - h * plan.row_tiles) * ROWS + r;
+  if (row >= a.tokens * a.group) return;
+  const int n = x.last - cta + 1;
+  // the first part is what CTA `cta` has at its end, the others what the CTAs behind it have at their beginnings
+  auto part = [&](int k) -> const float * { return plan.parts + (int64_t(cta + k) * 2 + (k == 0 ? 1 : 0)) * PART; };
+  float m = -1e30f, l = 0.0f, mk[(MOST + kThreads - 1) / kThreads], lk[(MOST + kThreads - 1) / kThreads];
+#pragma unroll
+  for (int i = 0; i < (MOST + kThreads - 1) / kThreads; ++i) {
+    const int k = tid + i * kThreads;
+    mk[i] = k < n ? part(k)[r] : -1e30f;
+    lk[i] = k < n ? part(k)[ROWS + r] : 0.0f;
+    m = fmaxf(m, mk[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[0][warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red[0][w]);
+#pragma unroll
+  for (int i = 0; i < (MOST + kThreads - 1) / kThreads; ++i) {
+    const int k = tid + i * kThreads;
+    const float w = exp2_approx(mk[i] - m);
+    if (k < n) weights[k] = w;
+    l = fmaf(w, lk[i], l);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
+  const int c = tid % COLS, share = tid / COLS;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = share; k < n; k += SHARES) {
+    const float w = weights[k];
+    const float4 v = reinterpret_cast<const float4 *>(part(k) + 2 * ROWS)[r * COLS + c];
+    o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+  }
+  sums[share][c] = o;
+  __syncthreads();
+  if (tid < COLS) {
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) l += red[1][w];
+    o = sums[0][tid];
+#pragma unroll
+    for (int i = 1; i < SHARES; ++i) {
+      const float4 v = sums[i][tid];
+      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    put_out<D>(a, seq, h, row, tid, o, m, l);
+  }
 }
 
 struct Sizes {
@@ -882,7 +968,7 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
   if ((e = cudaGetLastError()) != cudaSuccess || s.ctas == 1) return e;
   // The join starts while the last CTAs run, and waits for them.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(s.ctas);
+  cfg.gridDim = dim3(s.ctas, 8 * NT);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
