@@ -47,6 +47,8 @@ __device__ uint32_t g_fault = 0;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSms = 148;  // the grid never has more CTAs than these hold
+// Units of at most so many chunks, and no more of them than CTAs, get a CTA each: no list of places, no second kernel.
+constexpr int kDirectChunks = 2 * kWarps;
 
 template <int BITS, int D, int G, int NT>
 struct Form {
@@ -77,6 +79,7 @@ struct Loose {
 
 struct Plan {
   int ctas;          // of the launch
+  bool direct;       // a CTA for each unit
   int row_tiles;     // of a KV head's query rows
   float *parts;      // [ctas][2][kPart]: the unit that goes on from the CTA before, the one that goes on behind it
   float *heads;      // [ctas][kWarps][kPart]: the end of a unit that another warp began
@@ -85,7 +88,7 @@ struct Plan {
 
 // Positions that a sequence's new tokens see between them, as chunks.
 struct Span {
-  int len, first, chunks;  // first chunk; at least one, so that rows that see nothing are written too
+  int len, begin, first, chunks;  // length and first position; first chunk; at least one, so that rows that see nothing are written too
 };
 template <int CHUNK>
 AQ_DEVICE Span span_of(const AttentionArgs &a, int seq) {
@@ -94,7 +97,7 @@ AQ_DEVICE Span span_of(const AttentionArgs &a, int seq) {
   const int64_t end = max(int64_t(0), min(len, cap));
   const int64_t lo = a.window ? max(int64_t(0), min(end, len - a.tokens + 1 - a.window)) : 0;
   const int first = static_cast<int>(lo / CHUNK);
-  return Span{len32, first, max(1, static_cast<int>((end + CHUNK - 1) / CHUNK) - first)};
+  return Span{len32, static_cast<int>(lo), first, max(1, static_cast<int>((end + CHUNK - 1) / CHUNK) - first)};
 }
 
 AQ_DEVICE void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -196,6 +199,17 @@ AQ_DEVICE void load_queries(Queries<BITS, D, G, NT> &x, const AttentionArgs &a, 
         }
       }
   }
+}
+
+// Brings a unit's query rows near: a lane asks for one of their 128-byte lines.
+template <int D, int NT>
+AQ_DEVICE void prefetch_queries(const AttentionArgs &a, int seq, int h, int row0) {
+  constexpr int LINES = D / 64;
+  const int lane = threadIdx.x & 31, r = row0 + lane / LINES;
+  if (lane >= 8 * NT * LINES || r >= a.tokens * a.group) return;
+  const int j = a.tokens == 1 ? 0 : r / a.group, i = r - j * a.group;
+  const uint16_t *q = a.q + seq * a.q_stride[0] + j * a.q_stride[1] + (h * a.group + i) * a.q_stride[2];
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane % LINES * 64));
 }
 
 template <int BITS, int D, int G, int NT>
@@ -316,10 +330,13 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
     const uint8_t *k0 = tile + tok * F::kRow + t * (KW * 4), *k1 = k0 + 8 * F::kRow;
     const uint8_t *meta = tile + 2 * kTile * F::kRow + tok * F::kMeta;
     uint32_t sk[2][NG];
-    lds<NG>(sk[0], meta);
-    lds<NG>(sk[1], meta + 8 * F::kMeta);
-    lds<NG>(sv[i][0], meta + F::kMeta / 2);
-    lds<NG>(sv[i][1], meta + 8 * F::kMeta + F::kMeta / 2);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t kv[2 * NG];  // a token's pairs: K's, then V's
+      lds<2 * NG>(kv, meta + half * 8 * F::kMeta);
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi) sk[half][gi] = kv[gi], sv[i][half][gi] = kv[NG + gi];
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -397,14 +414,15 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
   // --- the running reference.  A weight is 2^(x - m): m is the row's maximum so far + e - 15, where every V scale so far is
   // below 2^e, so that (weight * scale) stays below 2^15 and is a normal fp16 down to 2^-29 of that: what rounds to nothing
   // is smaller than a 2^-39th of the largest
-  uint32_t top = 0;
+  __half2 top = __half2half2(__ushort_as_half(0));  // (scale, bias): the low half is what counts; a NaN is passed over
 #pragma unroll
   for (int i = 0; i < CT; ++i)
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
-      for (int gi = 0; gi < NG; ++gi) top = max(top, sv[i][half][gi] & 0x7FFFu);
-  const int e = max(st.e, static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 10) - 14);
+      for (int gi = 0; gi < NG; ++gi) top = __hmax2(top, *reinterpret_cast<const __half2 *>(&sv[i][half][gi]));
+  const uint32_t top_bits = __half_as_ushort(__low2half(top));
+  const int e = max(st.e, static_cast<int>(__reduce_max_sync(0xffffffffu, top_bits) >> 10) - 14);
   float mx[NT][2];
   bool more = e > st.e;
 #pragma unroll
@@ -640,6 +658,10 @@ AQ_DEVICE void put_out(const AttentionArgs &a, int seq, int h, int r, int c, flo
 }
 
 // A warp's place in the list of chunks: units are numbered sequence by sequence, heads and then row tiles within one.
+// A unit counts kUnitCost chunks more than it has, in front of its first: reading its queries and writing its result take
+// a warp about as long as a chunk of 32 tokens (2 us beside 2.3 us with all SMs busy).
+constexpr int kUnitCost = 1;
+
 template <int CHUNK>
 struct Cursor {
   int seq, head, row_tile;
@@ -673,13 +695,27 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
     fence_barrier_init();
   }
   if (threadIdx.x == 0) abort_flag = 0;
-  // --- how many chunks there are, and where this warp's run begins: thread i counts its share of the sequences
   const int units = a.c.heads * plan.row_tiles;  // of a sequence
-  const int per = (a.c.batch + kThreads - 1) / kThreads;
-  {
+  Cursor<CHUNK> cur;
+  int begin, end, share;  // the warp's run, in places of the list; places of a warp
+  if (plan.direct) {
+    // A CTA has one unit, and its warps equal runs of that.
+    __syncthreads();
+    cur.seq = blockIdx.x / units;
+    const int unit = blockIdx.x - cur.seq * units;
+    cur.head = unit / plan.row_tiles;
+    cur.row_tile = unit - cur.head * plan.row_tiles;
+    cur.span = span_of<CHUNK>(a, cur.seq);
+    share = (cur.span.chunks + kWarps - 1) / kWarps;
+    cur.chunk = warp * share;
+    begin = min(cur.span.chunks, cur.chunk);
+    end = min(cur.span.chunks, begin + share);
+  } else {
+    // How many places there are, and where this warp's run begins: thread i counts its share of the sequences.
+    const int per = (a.c.batch + kThreads - 1) / kThreads;
     int n = 0;
     for (int b = threadIdx.x * per; b < min(a.c.batch, (static_cast<int>(threadIdx.x) + 1) * per); ++b)
-      n += span_of<CHUNK>(a, b).chunks;
+      n += span_of<CHUNK>(a, b).chunks + kUnitCost;
     int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -689,72 +725,81 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
     if (lane == 31) warp_sums[warp] = incl;
     __syncthreads();
     int before = 0;
-    for (int w = 0; w < warp; ++w) before += warp_sums[w];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) before += w < warp ? warp_sums[w] : 0;
     sums[threadIdx.x + 1] = before + incl;
     if (threadIdx.x == 0) sums[0] = 0;
     __syncthreads();
-  }
-  const int total = sums[kThreads] * units;
-  const int share = max(1, (total + plan.ctas * kWarps - 1) / (plan.ctas * kWarps));
-  const int begin = static_cast<int>(min(int64_t(total), (int64_t(blockIdx.x) * kWarps + warp) * share));
-  const int end = static_cast<int>(min(int64_t(total), int64_t(begin) + share));
-  if (lane == 0) head_unit[warp] = tail_unit[warp] = -1;
-  if (begin < end) {
-    Cursor<CHUNK> cur;
-    {
-      int lo = 0, hi = kThreads;  // the last share of sequences that begins at or before this run
+    const int total = sums[kThreads] * units;
+    share = max(1, (total + plan.ctas * kWarps - 1) / (plan.ctas * kWarps));
+    const int from = static_cast<int>(min(int64_t(total), (int64_t(blockIdx.x) * kWarps + warp) * share));
+    const int to = static_cast<int>(min(int64_t(total), int64_t(from) + share));
+    begin = end = 0;
+    if (from < to) {
+      int lo = 0, hi = kThreads;  // the last share of sequences that begins at or before the run
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (sums[mid] * units <= begin) lo = mid;
+        if (sums[mid] * units <= from) lo = mid;
         else hi = mid;
       }
       int at = sums[lo] * units;
       cur.seq = lo * per;
       cur.span = span_of<CHUNK>(a, cur.seq);
-      while (begin - at >= cur.span.chunks * units) {
-        at += cur.span.chunks * units;
+      while (from - at >= (cur.span.chunks + kUnitCost) * units) {
+        at += (cur.span.chunks + kUnitCost) * units;
         cur.span = span_of<CHUNK>(a, ++cur.seq);
       }
-      const int unit = (begin - at) / cur.span.chunks;
-      cur.chunk = (begin - at) - unit * cur.span.chunks;
+      const int places = cur.span.chunks + kUnitCost, unit = (from - at) / places, place = (from - at) - unit * places;
       cur.head = unit / plan.row_tiles;
       cur.row_tile = unit - cur.head * plan.row_tiles;
+      cur.chunk = max(0, place - kUnitCost);
+      // the run's chunks are those at the places [begin, end), the first of them being cur.chunk
+      begin = from + (cur.chunk + kUnitCost - place);
+      end = to;
     }
+  }
+  if (lane == 0) head_unit[warp] = tail_unit[warp] = -1;
+  if (begin < end) {
     uint8_t *ring = smem + warp * F::kRing;
     // --- the copies: `ahead` runs kStages chunks in front of cur.  Lane i < CT looks after a chunk's tile i: it loads the
     // table's entry one chunk early and looks at it when the copies are issued
     Cursor<CHUNK> ahead = cur;
-    int left = end - begin, flying = 0, stage_in = 0;  // chunks not yet issued, and issued but not yet used
-    uint32_t valid_bits = 0;               // CT bits for each stage
-    int page = 0;
+    int left = end - begin, flying = 0, stage_in = 0;  // places not yet issued; chunks issued but not yet used
+    uint32_t valid_bits = 0;                           // CT bits for each chunk in flight, the oldest lowest
+    int page = 0, pos_in = (ahead.span.first + ahead.chunk) * CHUNK + lane * kTile;
     bool needed = false;
+    const int page_mask = (1 << a.c.page_shift) - 1;
     auto look_up = [&]() {
       // (only tiles that some row sees: entries in front of a window may hold anything)
-      const int pos = (ahead.span.first + ahead.chunk) * CHUNK + lane * kTile, e = pos >> a.c.page_shift;
-      needed = lane < CT && pos < ahead.span.len && e < a.c.width &&
-               (a.window == 0 || pos + kTile > int64_t(ahead.span.len) - a.tokens + 1 - a.window);
+      const int e = pos_in >> a.c.page_shift;
+      needed = lane < CT && pos_in < ahead.span.len && e < a.c.width && pos_in + kTile > ahead.span.begin;
       if (needed) page = __ldg(a.c.table + int64_t(ahead.seq) * a.c.width + e);
     };
     auto issue = [&]() {
       const bool there = needed && static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.pages);
       const uint32_t ok = __ballot_sync(0xffffffffu, there);
-      valid_bits = (valid_bits & ~(((1u << CT) - 1u) << (stage_in * CT))) | ok << (stage_in * CT);
+      valid_bits |= ok << (flying * CT);
       uint64_t *bar = &bars[warp][stage_in];
       if (lane == 0) mbar_arrive_expect_tx(bar, __popc(ok) * F::kTileBytes);
       __syncwarp();
       if (there) {
-        const int pos = (ahead.span.first + ahead.chunk) * CHUNK + lane * kTile;
-        bulk_g2s(ring + stage_in * F::kStage + lane * F::kTileBytes,
-                 a.c.data + tile_index(a.c, page, ahead.head, pos) * F::kTileBytes, F::kTileBytes, bar);
+        const int64_t tile = ((int64_t(page) * a.c.heads + ahead.head) << (a.c.page_shift - 4)) + ((pos_in & page_mask) >> 4);
+        bulk_g2s(ring + stage_in * F::kStage + lane * F::kTileBytes, a.c.data + tile * F::kTileBytes, F::kTileBytes, bar);
       } else if (needed) {
         atomicOr(&g_fault, kFaultBadIndex);
       }
       if (++stage_in == F::kStages) stage_in = 0;
       ++flying;
-      if (--left > 0) {
-        if (++ahead.chunk == ahead.span.chunks) ahead.next_unit(a, plan.row_tiles);
-        look_up();
+      pos_in += CHUNK;
+      --left;
+      if (++ahead.chunk == ahead.span.chunks) {
+        left -= kUnitCost;
+        if (left <= 0) return;
+        ahead.next_unit(a, plan.row_tiles);
+        pos_in = ahead.span.first * CHUNK + lane * kTile;
+        prefetch_queries<D, NT>(a, ahead.seq, ahead.head, ahead.row_tile * F::kRows);
       }
+      if (left > 0) look_up();
     };
     look_up();
     Queries<BITS, D, G, NT> queries;
@@ -775,7 +820,8 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
         if (!ok) break;
         --flying;
         const uint8_t *tiles = ring + stage * F::kStage;
-        const uint32_t valid = valid_bits >> (stage * CT) & ((1u << CT) - 1u);
+        const uint32_t valid = valid_bits & ((1u << CT) - 1u);
+        valid_bits >>= CT;
         if (valid == (1u << CT) - 1u && pos >= st.lo_all && pos + CHUNK <= st.hi_all) run_chunk<true>(st, tiles, pos, valid);
         else run_chunk<false>(st, tiles, pos, valid);
         __syncwarp();
@@ -783,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
         if (++stage == F::kStages) stage = 0, parity ^= 1;
       }
       if (!ok) break;
-      at += take;
+      at += take;  // the place behind this unit's part, or behind the unit
       finish_unit(st);
       const int id = cur.seq * units + cur.head * plan.row_tiles + cur.row_tile;
       if (first == 0 && take == cur.span.chunks) {
@@ -795,11 +841,12 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
         write_part(st, reinterpret_cast<float *>(ring));
         if (lane == 0) {
           tail_unit[warp] = id;
-          tail_end[warp] = at - first - take + cur.span.chunks;
+          tail_end[warp] = at - first - take + cur.span.chunks;  // the place behind the unit
           tail_starts[warp] = first == 0;
         }
       }
       if (cur.span.len > (int64_t(a.c.width) << a.c.page_shift) && lane == 0) atomicOr(&g_fault, kFaultBadIndex);
+      at += kUnitCost;  // the next unit's first chunk
       if (at >= end) break;
       cur.next_unit(a, plan.row_tiles);
       load_queries(queries, a, cur.seq, cur.head, cur.row_tile * F::kRows);
@@ -848,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
       }
     }
   }
-  if (threadIdx.x == 0) plan.loose[blockIdx.x] = loose;
+  if (threadIdx.x == 0 && !plan.direct) plan.loose[blockIdx.x] = loose;
 }
 
 // Joins the units that several CTAs have a part of: block (i, r) takes row r of the one that starts in CTA i's run and
@@ -921,6 +968,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 
 struct Sizes {
   int ctas, row_tiles;
+  bool direct;
   size_t parts, heads, loose, bytes;  // offsets of the workspace's parts, and its size
 };
 
@@ -929,15 +977,17 @@ Sizes sizes_of(const AttentionArgs &a) {
   using F = Form<BITS, D, G, NT>;
   Sizes s;
   s.row_tiles = (a.tokens * a.group + F::kRows - 1) / F::kRows;
-  // chunks that there can be; a CTA has one for each of its warps at least
-  int64_t most = ((int64_t(a.c.width) << a.c.page_shift) + F::kCT * kTile - 1) / (F::kCT * kTile) + 1;
+  const int64_t units = int64_t(a.c.batch) * a.c.heads * s.row_tiles, slots = int64_t(kSms) * F::kCtas;
+  // chunks that a unit can have
+  int64_t most = ((int64_t(a.c.width) << a.c.page_shift) + F::kCT * kTile - 1) / (F::kCT * kTile);
   if (a.window) most = std::min<int64_t>(most, (int64_t(a.window) + a.tokens) / (F::kCT * kTile) + 2);
-  const int64_t ctas = (int64_t(a.c.batch) * a.c.heads * s.row_tiles * most + kWarps - 1) / kWarps;
-  s.ctas = static_cast<int>(std::min<int64_t>(ctas, int64_t(kSms) * F::kCtas));
+  s.direct = units <= slots && most <= kDirectChunks;
+  // a CTA has a place for each of its warps at least
+  s.ctas = static_cast<int>(s.direct ? units : std::min<int64_t>((units * (most + kUnitCost) + kWarps - 1) / kWarps, slots));
   s.parts = 0;
-  s.heads = s.parts + size_t(s.ctas) * 2 * F::kPart * 4;
+  s.heads = s.parts + (s.direct ? 0 : size_t(s.ctas) * 2 * F::kPart * 4);
   s.loose = s.heads + size_t(s.ctas) * kWarps * F::kPart * 4;
-  s.bytes = s.loose + size_t(s.ctas) * sizeof(Loose);
+  s.bytes = s.loose + (s.direct ? 0 : size_t(s.ctas) * sizeof(Loose));
   return s;
 }
 
@@ -960,12 +1010,13 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   Plan plan;
   plan.ctas = s.ctas;
+  plan.direct = s.direct;
   plan.row_tiles = s.row_tiles;
   plan.parts = reinterpret_cast<float *>(ws + s.parts);
   plan.heads = reinterpret_cast<float *>(ws + s.heads);
   plan.loose = reinterpret_cast<Loose *>(ws + s.loose);
   kern<<<s.ctas, kThreads, kBytes, stream>>>(a, plan);
-  if ((e = cudaGetLastError()) != cudaSuccess || s.ctas == 1) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || s.direct || s.ctas == 1) return e;
   // The join starts while the last CTAs run, and waits for them.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(s.ctas, 8 * NT);
