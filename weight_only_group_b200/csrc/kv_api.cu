@@ -46,8 +46,7 @@ aq_status check_cache(const aq_kv_cache *c, aq::kv::Cache *out) {
 
 // Rows of append and read: AQ_OK, or the status to return.
 aq_status check_rows(const aq_kv_cache *c, int64_t rows, const int32_t *offsets) {
-  // (one thread for each 8 values, 2^31 - 1 blocks of 256 threads at most)
-  if (rows < 0 || rows > kMaxInt || rows * c->heads > (kMaxInt * 256) / (c->D / 8)) return AQ_ERR_INVALID_ARG;
+  if (rows < 0 || rows > kMaxInt) return AQ_ERR_INVALID_ARG;
   if (!aligned(offsets, 4)) return AQ_ERR_ALIGNMENT;
   if (!offsets && c->batch > 0 && rows % c->batch != 0) return AQ_ERR_INVALID_ARG;
   return AQ_OK;
