@@ -80,6 +80,26 @@ def test_append_from_a_fused_projection():
     assert torch.equal(again, first)
 
 
+@pytest.mark.parametrize("bits", (4, 8))
+def test_rows_that_begin_on_16_bytes(bits):
+    """k, v and the outputs of a read on 16 bytes but not on 32, and rows an odd number of 16 bytes apart."""
+    D, G, H, n = 128, 32, 3, 11
+    c = cache([20], heads=H, page_size=16, D=D, G=G, bits=bits, seed=6)
+    data, table, ln = on_gpu(c)
+    flat = torch.randn(2 * n * (H * D + 8) + 8, device="cuda").bfloat16()[8:]
+    k, v = flat.view(2, n, H * D + 8)[:, :, :H * D].unflatten(2, (H, D))
+    assert k.data_ptr() % 32 == 16
+    aq.aq_kv_append(data, k, v, table, ln, G, bits, offsets=_gpu([0, n]))
+    ref.append(c, bits_of(k), bits_of(v), [0, n])
+    assert np.array_equal(data.cpu().numpy(), c.data)
+    room = torch.zeros(2, n * H * D + 8, dtype=torch.bfloat16, device="cuda")
+    out = tuple(x[8:].view(n, H, D) for x in room)
+    aq.aq_kv_read(data, table, ln, n, D, G, bits, offsets=_gpu([0, n]), out=out)
+    for x, y in zip(out, ref.read(c, n, [0, n])):
+        assert np.array_equal(bits_of(x), y)
+    assert not room[:, :8].any()
+
+
 def test_rows_of_no_sequence_stay():
     """Offsets that begin behind row 0 and end before the last: the rows around them are nobody's."""
     D, G, bits = 64, 64, 8
@@ -132,6 +152,22 @@ def test_extreme_rows():
         aq.aq_kv_append(data, to_gpu(k), to_gpu(k[::-1]), table, ln, G, bits, offsets=_gpu([0, 8]))
         ref.append(c, k, k[::-1], [0, 8])
         assert np.array_equal(data.cpu().numpy(), c.data)
+
+
+@pytest.mark.parametrize("bits", (4, 8))
+def test_quotients_at_and_beside_ties(bits):
+    """Inputs of few bits on every scale: quotients that lie on the middle between two codes, or an ulp of it away."""
+    D, G, n = 256, 32, 600
+    rng = np.random.default_rng(bits)
+    step = 2.0 ** rng.integers(-9, 4, (n, 1, D // G, 1))
+    x = rng.integers(-255, 256, (n, 1, D // G, G)) * step
+    x[::3] += rng.integers(-128, 129, (len(x[::3]), 1, D // G, 1)) * 2.0 ** rng.integers(-12, 3, (len(x[::3]), 1, D // G, 1))
+    k = bf16_bits(x.reshape(n, 1, D))
+    c = cache([n], heads=1, page_size=128, D=D, G=G, bits=bits, seed=3)
+    data, table, ln = on_gpu(c)
+    aq.aq_kv_append(data, to_gpu(k), to_gpu(k[::-1]), table, ln, G, bits, offsets=_gpu([0, n]))
+    ref.append(c, k, k[::-1], [0, n])
+    assert np.array_equal(data.cpu().numpy(), c.data)
 
 
 # ------------------------------------------------------------------------------ attention

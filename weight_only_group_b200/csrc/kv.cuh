@@ -46,6 +46,7 @@ struct AppendArgs {
   const int32_t *offsets;        // [batch + 1], or null: `rows_per_seq` rows each
   int64_t rows;
   int rows_per_seq;
+  bool wide;  // every thread's 16 values begin on 32 bytes
 };
 
 struct ReadArgs {
@@ -54,6 +55,7 @@ struct ReadArgs {
   const int32_t *offsets;
   int64_t rows;
   int rows_per_seq;
+  bool wide;  // every thread's 16 values begin on 32 bytes
 };
 
 struct AttentionArgs {

@@ -83,6 +83,8 @@ aq_status aq_kv_append(const aq_kv_cache *cache, const uint16_t *k_bf16, int64_t
   a.offsets = offsets;
   a.rows = rows;
   a.rows_per_seq = static_cast<int>(rows / cache->batch);
+  a.wide = aligned(k_bf16, 32) && aligned(v_bf16, 32) &&
+           (k_row_stride | k_head_stride | v_row_stride | v_head_stride) % 16 == 0;
   return aq::api_from_cuda(aq::kv::launch_append(a, cache->D, cache->G, cache->bits, stream));
 }
 
@@ -100,6 +102,7 @@ aq_status aq_kv_read(const aq_kv_cache *cache, int64_t rows, const int32_t *offs
   a.offsets = offsets;
   a.rows = rows;
   a.rows_per_seq = static_cast<int>(rows / cache->batch);
+  a.wide = aligned(k_bf16, 32) && aligned(v_bf16, 32);
   return aq::api_from_cuda(aq::kv::launch_read(a, cache->D, cache->G, cache->bits, stream));
 }
 

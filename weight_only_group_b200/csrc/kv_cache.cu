@@ -9,10 +9,11 @@
 //
 // Both kernels move each byte once.  A warp takes one row of k or of v: where the
 // row lies (its sequence, position and page) is found once and holds for all heads,
-// which the warp then goes through, a thread having 8 values at a time (a 16-byte
-// bf16 access on one side, one or two code words on the other).  Eight rows of a
-// block lie next to each other in the same tiles.  The G / 8 threads of a group
-// are neighbouring lanes and join their minimum and maximum with shuffles.
+// which the warp then goes through, a thread having 16 values of K and of V at a
+// time (32 bytes of bf16 on one side, one access where they are aligned to 32; two
+// or four code words on the other).  Eight rows of a block lie next to each other
+// in the same tiles.  The G / 16 threads of a group are neighbouring lanes and join
+// their minimum and maximum with shuffles.
 #include "kv.cuh"
 
 namespace aq {
@@ -23,20 +24,24 @@ __device__ uint32_t g_cache_fault = 0;
 namespace {
 
 // The sequence that row r belongs to and the row's position in it: a sequence's
-// rows are its last tokens.  False: no sequence has the row.
+// rows are its last tokens.  False: no sequence has the row.  One row for a warp.
 AQ_DEVICE bool locate(const Cache &c, const int32_t *offsets, int rows_per_seq, int r, int &seq, int &pos) {
+  const int lane = threadIdx.x & 31;
   int end;
   if (offsets) {
-    int lo = 0, hi = c.batch;  // the last b with offsets[b] <= r, or 0
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(offsets + mid) <= r) lo = mid;
-      else hi = mid;
+    // the last b with offsets[b] <= r, or 0: the lanes look at 32 entries at a time
+    int lo = 0, n = c.batch;
+    while (n > 1) {
+      const int step = (n + 31) >> 5, at = lane * step;
+      const uint32_t below = __ballot_sync(0xffffffffu, at < n && __ldg(offsets + lo + at) <= r) | 1u;
+      const int k = 31 - __clz(below);
+      lo += k * step;
+      n = min(step, n - k * step);
     }
     seq = lo;
-    if (r < __ldg(offsets + lo)) return false;
+    const int begin = __ldg(offsets + lo);
     end = __ldg(offsets + lo + 1);
-    if (r >= end) return false;
+    if (r < begin || r >= end) return false;
   } else {
     seq = r / rows_per_seq;
     end = (seq + 1) * rows_per_seq;
@@ -54,6 +59,35 @@ AQ_DEVICE int page_of(const Cache &c, int seq, int pos) {
 }
 
 constexpr int kRowsPerBlock = 8;  // a warp for each
+constexpr int kVals = 16;         // values of a thread
+
+struct Bf16x16 {
+  uint32_t w[8];
+};
+// 32 bytes: one access where the address allows it (wide, the same for the whole launch).
+AQ_DEVICE Bf16x16 load16(const uint16_t *p, bool wide) {
+  Bf16x16 x;
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]),
+                   "=r"(x.w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = ldg_nc16(p), b = ldg_nc16(p + 8);
+    x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w, x.w[4] = b.x, x.w[5] = b.y, x.w[6] = b.z, x.w[7] = b.w;
+  }
+  return x;
+}
+AQ_DEVICE void store16(uint16_t *p, const uint4 &a, const uint4 &b, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                 "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(p)[0] = a;
+    reinterpret_cast<uint4 *>(p)[1] = b;
+  }
+}
 
 // The row of this warp, and what all its heads share.
 struct Place {
@@ -70,59 +104,49 @@ AQ_DEVICE bool find(const Cache &c, const int32_t *offsets, int rows_per_seq, in
   return true;
 }
 
-// Codes of 8 values of a group as words, by the definition: rint of the quotient, an IEEE division.
+// Codes of 16 values of a group as words, two values an instruction where there is one for two.  The definition's IEEE
+// quotient d / s comes from the correctly rounded reciprocal y of s by Markstein's theorem (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990): with q = rn(d y), which is within an ulp, and the
+// residual r = d - q s, which one fma gives exactly, rn(q + r y) is the correctly rounded quotient.  s is fp16, so nothing
+// here overflows, and where d is so small that r underflows the code is 0 either way.  (A product with y alone would not
+// do: inputs of few bits make exact ties common.)  Adding 1.5 2^23 rounds to an integer, half to even, and leaves it in
+// the low bits; clamping to integers may as well come before.
 template <int BITS>
-AQ_DEVICE void encode_exact(const float2 (&v)[4], float sf, float bf, uint32_t (&out)[BITS / 4]) {
-  constexpr float qmax = float((1 << BITS) - 1);
-#pragma unroll
-  for (int i = 0; i < BITS / 4; ++i) out[i] = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float t = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(j & 1 ? v[j / 2].y : v[j / 2].x, bf), sf)), 0.0f), qmax);
-    const uint32_t q = sf == 0.0f ? 0u : static_cast<uint32_t>(t);
-    out[j * BITS / 32] |= q << (j * BITS % 32);
-  }
-}
-
-// The same with a product in the division's place: t = qmax * sat(d * (1 / (qmax s))), two values an instruction where
-// there is one for two.  The reciprocal is within 2^-22 of its value (4 bits; 2^-24 at 8 bits, where an exact one pays),
-// the product and the definition's own quotient within 2^-24 each, so where the code is not clamped t and the quotient
-// differ by less than 2^-21 16 = 2^-17 (3 2^-24 256 < 2^-14 at 8 bits), and their nearest integers are the same unless t
-// lies that close to the middle between two.  False: it does for some value, or s is 0 (one warp in 250; one in 30 at 8
-// bits).  Adding 1.5 2^23 rounds to an integer (half to even) and leaves it in the low bits.
-template <int BITS>
-AQ_DEVICE bool encode_fast(const float2 (&v)[4], float sf, float bf, uint32_t (&out)[BITS / 4]) {
+AQ_DEVICE void encode16(const uint32_t (&w)[8], float sf, float bf, uint32_t (&out)[BITS / 2]) {
   constexpr float qmax = float((1 << BITS) - 1), kMagic = 12582912.0f;
   constexpr uint32_t kMagicBits = 0x4B400000u;
   constexpr int PW = 32 / BITS;
-  const float inv = BITS == 4 ? __fdividef(1.0f, qmax * sf) : __frcp_rn(qmax * sf);
-  const float2 minus_b = make_float2(-bf, -bf), q2 = make_float2(qmax, qmax);
-  float far = 0.0f;
+  const float inv = __frcp_rn(sf);
+  const float2 y = make_float2(inv, inv), minus_s = make_float2(-sf, -sf), minus_b = make_float2(-bf, -bf);
   uint32_t extra = 0;
 #pragma unroll
   for (int j = 0; j < PW; ++j) extra += kMagicBits << (j * BITS);
 #pragma unroll
-  for (int i = 0; i < BITS / 4; ++i) out[i] = 0u - extra;  // (the magic's own bits, taken off beforehand)
+  for (int i = 0; i < BITS / 2; ++i) out[i] = 0u - extra;  // (the magic's own bits, taken off beforehand)
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float2 t = fadd2(v[j], minus_b);
-    t = make_float2(__saturatef(t.x * inv), __saturatef(t.y * inv));
-    const float2 m = ffma2(t, q2, make_float2(kMagic, kMagic));
-    const float2 whole = fadd2(m, make_float2(-kMagic, -kMagic));
-    const float2 r = ffma2(t, q2, make_float2(-whole.x, -whole.y));
-    far = fmaxf(far, fmaxf(fabsf(r.x), fabsf(r.y)));
+  for (int j = 0; j < kVals / 2; ++j) {
+    const float2 d = fadd2(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), minus_b);
+    const float2 q = __fmul2_rn(d, y), r = ffma2(q, minus_s, d);
+    float2 t = ffma2(r, y, q);
+    t = make_float2(fminf(fmaxf(t.x, 0.0f), qmax), fminf(fmaxf(t.y, 0.0f), qmax));
+    const float2 m = fadd2(t, make_float2(kMagic, kMagic));
     out[2 * j / PW] += (__float_as_uint(m.x) << (2 * j % PW * BITS)) + (__float_as_uint(m.y) << ((2 * j + 1) % PW * BITS));
   }
-  return far < 0.5f - (BITS == 4 ? 0x1p-17f : 0x1p-14f) && sf != 0.0f;
+  if (sf == 0.0f) {
+#pragma unroll
+    for (int i = 0; i < BITS / 2; ++i) out[i] = 0;
+  }
 }
 
-// 8 bf16 values of a row, the rest of their group in the GL neighbouring lanes -> codes, and the group's (scale, bias).
+// 16 bf16 values of a row, the rest of their group in the GL neighbouring lanes -> codes, and the group's (scale, bias).
 // All lanes of the warp take part.
 template <int BITS, int GL>
-AQ_DEVICE __half2 encode(const uint32_t (&w)[4], uint32_t (&out)[BITS / 4]) {
+AQ_DEVICE __half2 encode(const uint32_t (&w)[8], uint32_t (&out)[BITS / 2]) {
   const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(w);
   __nv_bfloat162 lo = __hmin2(__hmin2(x[0], x[1]), __hmin2(x[2], x[3]));
   __nv_bfloat162 hi = __hmax2(__hmax2(x[0], x[1]), __hmax2(x[2], x[3]));
+  lo = __hmin2(lo, __hmin2(__hmin2(x[4], x[5]), __hmin2(x[6], x[7])));
+  hi = __hmax2(hi, __hmax2(__hmax2(x[4], x[5]), __hmax2(x[6], x[7])));
 #pragma unroll
   for (int o = 1; o < GL; o <<= 1) {
     lo = __hmin2(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -136,56 +160,62 @@ AQ_DEVICE __half2 encode(const uint32_t (&w)[4], uint32_t (&out)[BITS / 4]) {
   const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), qmax));
   const __half b16 = __float2half_rn(mn);
   const float sf = __half2float(s16), bf = __half2float(b16);
-  float2 v[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
-  if (!encode_fast<BITS>(v, sf, bf, out)) encode_exact<BITS>(v, sf, bf, out);
+  encode16<BITS>(w, sf, bf, out);
   return __halves2half2(s16, b16);
 }
 
 template <int BITS, int G>
 __global__ void __launch_bounds__(kRowsPerBlock * 32) append_kernel(const __grid_constant__ AppendArgs a, int log_lanes) {
-  constexpr int GL = G / 8;  // lanes of a group
-  const int D = 8 << log_lanes, lane = threadIdx.x & 31, heads_at_once = 32 >> log_lanes;
+  constexpr int GL = G / kVals;  // lanes of a group
+  const int D = kVals << log_lanes, lane = threadIdx.x & 31, heads_at_once = 32 >> log_lanes;
   const Cache &c = a.c;
+  const int l = lane & ((1 << log_lanes) - 1);
+  // this lane's place among the first heads, and the way to the next: blockIdx.y has every gridDim.y-th run of heads
+  int h = blockIdx.y * heads_at_once + (lane >> log_lanes);
+  const int stride = gridDim.y * heads_at_once;
+  // the first values are on their way while the row's place is looked up, the next ones while these are quantised
+  const int64_t row = int64_t(blockIdx.x) * kRowsPerBlock + (threadIdx.x >> 5);
+  const uint16_t *src[2];
+  Bf16x16 raw[2] = {};
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    src[w] = a.src[w] + row * a.row_stride[w] + h * a.head_stride[w] + l * kVals;
+    if (row < a.rows && h < c.heads) raw[w] = load16(src[w], a.wide);
+  }
   Place p;
   if (!find(c, a.offsets, a.rows_per_seq, a.rows, p) || p.pos < 0) return;
   if (p.page < 0) {
     if (lane == 0) atomicOr(&g_cache_fault, kFaultBadIndex);
     return;
   }
-  const int rb = row_bytes(D, BITS), in = p.pos & (kTile - 1), l = lane & ((1 << log_lanes) - 1);
+  const int rb = row_bytes(D, BITS), in = p.pos & (kTile - 1);
   const int64_t head_bytes = int64_t(token_bytes(D, G, BITS)) << c.page_shift;
-  // this lane's place among the first heads, and the way to the next: blockIdx.y has every gridDim.y-th run of heads
-  int h = blockIdx.y * heads_at_once + (lane >> log_lanes);
-  const int stride = gridDim.y * heads_at_once;
-  uint8_t *codes = c.data + tile_index(c, p.page, 0, p.pos) * tile_bytes(D, G, BITS) + h * head_bytes + in * rb + l * BITS;
-  const int meta = 2 * kTile * rb + (in * 2 * (D / G) + l / GL) * 4 - (in * rb + l * BITS);  // from codes
-  const uint16_t *src[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) src[w] = a.src[w] + p.row * a.row_stride[w] + h * a.head_stride[w] + l * 8;
+  uint8_t *codes = c.data + tile_index(c, p.page, 0, p.pos) * tile_bytes(D, G, BITS) + h * head_bytes + in * rb + l * (2 * BITS);
+  const int meta = 2 * kTile * rb + (in * 2 * (D / G) + l / GL) * 4 - (in * rb + l * (2 * BITS));  // from codes
   for (int left = (c.heads - static_cast<int>(blockIdx.y) * heads_at_once + stride - 1) / stride; left > 0; --left) {
     const bool active = h < c.heads;
-    uint4 raw[2];
-#pragma unroll
-    for (int w = 0; w < 2; ++w) raw[w] = active ? ldg_stream16(src[w]) : make_uint4(0u, 0u, 0u, 0u);
+    h += stride;
+    Bf16x16 next[2] = {};
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const uint32_t r[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-      uint32_t out[BITS / 4];
-      const __half2 sb = encode<BITS, GL>(r, out);
+      src[w] += stride * a.head_stride[w];
+      if (h < c.heads) next[w] = load16(src[w], a.wide);
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t out[BITS / 2];
+      const __half2 sb = encode<BITS, GL>(raw[w].w, out);
       if (active) {
         uint8_t *to = codes + w * kTile * rb;
         if constexpr (BITS == 4) {
-          *reinterpret_cast<uint32_t *>(to) = out[0];
-        } else {
           *reinterpret_cast<uint2 *>(to) = make_uint2(out[0], out[1]);
+        } else {
+          *reinterpret_cast<uint4 *>(to) = make_uint4(out[0], out[1], out[2], out[3]);
         }
         if (l % GL == 0) *reinterpret_cast<__half2 *>(codes + meta + w * (D / G) * 4) = sb;
       }
-      src[w] += stride * a.head_stride[w];
+      raw[w] = next[w];
     }
-    h += stride;
     codes += stride * head_bytes;
   }
 }
@@ -216,37 +246,39 @@ AQ_DEVICE uint4 decode(uint2 w, uint32_t sb) {
 
 template <int BITS, int G>
 __global__ void __launch_bounds__(kRowsPerBlock * 32) read_kernel(const __grid_constant__ ReadArgs a, int log_lanes) {
-  constexpr int GL = G / 8;
-  const int D = 8 << log_lanes, lane = threadIdx.x & 31, heads_at_once = 32 >> log_lanes;
+  constexpr int GL = G / kVals;
+  const int D = kVals << log_lanes, lane = threadIdx.x & 31, heads_at_once = 32 >> log_lanes;
   const Cache &c = a.c;
   Place p;
   if (!find(c, a.offsets, a.rows_per_seq, a.rows, p)) return;
   const int rb = row_bytes(D, BITS), in = p.pos & (kTile - 1), l = lane & ((1 << log_lanes) - 1);
   int h = blockIdx.y * heads_at_once + (lane >> log_lanes);
   const int stride = gridDim.y * heads_at_once;
-  const int64_t to = (int64_t(p.row) * c.heads + h) * D + l * 8, step = int64_t(stride) * D;
+  const int64_t to = (int64_t(p.row) * c.heads + h) * D + l * kVals, step = int64_t(stride) * D;
   uint16_t *dst[2] = {a.dst[0] + to, a.dst[1] + to};
   if (p.page < 0) {  // zeros
     if (p.pos >= 0 && lane == 0) atomicOr(&g_cache_fault, kFaultBadIndex);
     for (; h < c.heads; h += stride)
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
-        *reinterpret_cast<uint4 *>(dst[which]) = make_uint4(0u, 0u, 0u, 0u);
+        store16(dst[which], make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u), a.wide);
         dst[which] += step;
       }
     return;
   }
   const int64_t head_bytes = int64_t(token_bytes(D, G, BITS)) << c.page_shift, head_step = stride * head_bytes;
-  const uint8_t *codes = c.data + tile_index(c, p.page, 0, p.pos) * tile_bytes(D, G, BITS) + h * head_bytes + in * rb + l * BITS;
-  const uint8_t *meta = codes + 2 * kTile * rb + (in * 2 * (D / G) + l / GL) * 4 - (in * rb + l * BITS);
+  const uint8_t *codes = c.data + tile_index(c, p.page, 0, p.pos) * tile_bytes(D, G, BITS) + h * head_bytes + in * rb + l * (2 * BITS);
+  const uint8_t *meta = codes + 2 * kTile * rb + (in * 2 * (D / G) + l / GL) * 4 - (in * rb + l * (2 * BITS));
   const int v_codes = kTile * rb, v_meta = D / G * 4;
-  auto load = [&](uint2(&w)[2], uint32_t(&sb)[2]) {
-    if constexpr (BITS == 4) {
-      w[0].x = ldg_nc4(codes);
-      w[1].x = ldg_nc4(codes + v_codes);
-    } else {
-      w[0] = ldg_nc8(codes);
-      w[1] = ldg_nc8(codes + v_codes);
+  auto load = [&](uint4(&w)[2], uint32_t(&sb)[2]) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      if constexpr (BITS == 4) {
+        const uint2 x = ldg_nc8(codes + which * v_codes);
+        w[which] = make_uint4(x.x, x.y, 0u, 0u);
+      } else {
+        w[which] = ldg_nc16(codes + which * v_codes);
+      }
     }
     sb[0] = ldg_nc4(meta);
     sb[1] = ldg_nc4(meta + v_meta);
@@ -255,20 +287,23 @@ __global__ void __launch_bounds__(kRowsPerBlock * 32) read_kernel(const __grid_c
   };
   // the next heads' loads are under way while these are written
   if (h >= c.heads) return;
-  uint2 w[2];
+  uint4 w[2];
   uint32_t sb[2];
   load(w, sb);
   while (true) {
     h += stride;
     const bool more = h < c.heads;
-    uint2 w1[2];
+    uint4 w1[2];
     uint32_t sb1[2];
     if (more) load(w1, sb1);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      uint4 *at = reinterpret_cast<uint4 *>(dst[which]);
-      if constexpr (BITS == 4) *at = decode(w[which].x, sb[which]);
-      else *at = decode(w[which], sb[which]);
+      if constexpr (BITS == 4) {
+        store16(dst[which], decode(w[which].x, sb[which]), decode(w[which].y, sb[which]), a.wide);
+      } else {
+        store16(dst[which], decode(make_uint2(w[which].x, w[which].y), sb[which]),
+                decode(make_uint2(w[which].z, w[which].w), sb[which]), a.wide);
+      }
       dst[which] += step;
       w[which] = w1[which];
       sb[which] = sb1[which];
@@ -289,11 +324,11 @@ cudaError_t by_form(int G, int bits, A &&...args) {
   return Launch<8, 128>::run(args...);
 }
 
-int log_lanes(int D) { return D == 64 ? 3 : D == 128 ? 4 : 5; }
+int log_lanes(int D) { return D == 64 ? 2 : D == 128 ? 3 : 4; }
 
 // A block for every kRowsPerBlock rows, and their heads spread over more blocks until there are a few for each SM.
 dim3 grid_for(int64_t rows, int heads, int D) {
-  const int64_t blocks = (rows + kRowsPerBlock - 1) / kRowsPerBlock, at_once = 256 / D;
+  const int64_t blocks = (rows + kRowsPerBlock - 1) / kRowsPerBlock, at_once = 32 * kVals / D;
   const int64_t steps = (heads + at_once - 1) / at_once;
   int64_t spread = (4 * 148 + blocks - 1) / blocks;
   if (spread > steps) spread = steps;
