@@ -617,56 +617,77 @@ def aq_kv_cache(pages: int, heads: int, page_size: int, D: int, G: int, bits: in
     return torch.zeros((pages, heads, page_size, tb), dtype=torch.uint8, device=device)
 
 
-def _need_index(t: torch.Tensor, name: str, dev: torch.device, ndim: int) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != ndim or not t.is_contiguous():
+# (These calls are short and frequent: each check below is one attribute or method of a tensor, and none is made twice.)
+
+_Tensor, _U8, _I32, _BF16 = torch.Tensor, torch.uint8, torch.int32, torch.bfloat16
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _need_index(t, name: str, dev: int, ndim: int) -> int:
+    if not (isinstance(t, _Tensor) and t.dtype is _I32 and t.dim() == ndim and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {ndim}-D int32 tensor")
-    if t.device != dev:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the cache's device")
+    return t.data_ptr()
 
 
-def _kv(cache, table, lens, D: int, G: int, bits: int) -> _KVCache:
-    _need(cache, "cache", _BYTE, 4)
-    _need_index(table, "table", cache.device, 2)
-    _need_index(lens, "lens", cache.device, 1)
+def _kv(cache, table, lens, D: int, G: int, bits: int):
+    """The C descriptor of a cache and its sequences, and the cache's device."""
+    if not (isinstance(cache, _Tensor) and cache.dtype is _U8 and cache.dim() == 4 and cache.is_contiguous()
+            and cache.is_cuda):
+        _need(cache, "cache", _BYTE, 4)
+    dev = cache.get_device()
+    tp, lp = _need_index(table, "table", dev, 2), _need_index(lens, "lens", dev, 1)
     batch, width = table.shape
-    if lens.shape[0] != batch:
+    if len(lens) != batch:
         raise ValueError("table and lens disagree on the number of sequences")
     pages, heads, page_size, held = cache.shape
-    tb = lib().aq_kv_token_bytes(D, G, bits)
-    if tb == 0:
-        raise AqError(AQ_ERR_UNSUPPORTED, "a key-value cache")
+    tb = 2 * (D * bits // 8) + 8 * (D // G) if G > 0 else 0  # aq_kv_token_bytes, of a form that the call itself checks
     if held != tb:
+        if aq_kv_token_bytes(D, G, bits) == 0:
+            raise AqError(AQ_ERR_UNSUPPORTED, "a key-value cache")
         raise ValueError(f"a token of the cache has {held} bytes, one of D = {D}, G = {G}, {bits} bits has {tb}")
-    return _KVCache(cache.data_ptr(), pages, heads, page_size, D, G, bits, table.data_ptr(), lens.data_ptr(), batch,
-                    width)
+    return _KVCache(cache.data_ptr(), pages, heads, page_size, D, G, bits, tp, lp, batch, width), dev
 
 
-def _need_rows(t: torch.Tensor, name: str, dev: torch.device, shape) -> None:
+def _need_rows(t, name: str, dev: int, shape) -> None:
     """bf16 of this shape, strided, its last dimension contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+    if not isinstance(t, _Tensor) or t.dtype is not _BF16:
         raise TypeError(f"{name} must be a bfloat16 tensor")
-    if t.device != dev:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the cache's device")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    if t.stride(-1) != 1:
+    if t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
-def _step(t: torch.Tensor, i: int) -> int:
-    """Stride of a dimension; a dimension of one entry has none that counts."""
-    return t.stride(i) if t.shape[i] > 1 else 0
+def _steps(t):
+    """Strides; a dimension of one entry has none that counts."""
+    st, sh = t.stride(), t.shape
+    return st if 1 not in sh else tuple(0 if n == 1 else s for s, n in zip(st, sh))
 
 
-def _need_offsets(offsets, dev: torch.device, batch: int, rows: int) -> int:
+def _need_offsets(offsets, dev: int, batch: int, rows: int) -> int:
     if offsets is None:
         if batch and rows % batch:
             raise ValueError("without offsets every sequence has as many rows: rows must be a multiple of the batch")
         return 0
-    _need_index(offsets, "offsets", dev, 1)
-    if offsets.shape[0] != batch + 1:
+    p = _need_index(offsets, "offsets", dev, 1)
+    if len(offsets) != batch + 1:
         raise ValueError("offsets must have one entry more than there are sequences")
-    return offsets.data_ptr()
+    return p
+
+
+def _call(fn, what: str, dev: int, *args) -> None:
+    """fn(*args, stream) on a device and its current stream."""
+    if dev == _current_device():
+        rc = fn(*args, _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc:
+        raise AqError(rc, what)
 
 
 def aq_kv_append(cache, k, v, table, lens, G: int, bits: int, offsets: torch.Tensor | None = None) -> None:
@@ -675,46 +696,46 @@ def aq_kv_append(cache, k, v, table, lens, G: int, bits: int, offsets: torch.Ten
     table int32 [batch, width]: the pages of each sequence; lens int32 [batch]: lengths with the new tokens counted;
     offsets int32 [batch + 1]: rows offsets[b] .. offsets[b + 1] - 1 are the last tokens of sequence b (None: as many
     rows for each).  See aq_kv_append in include/aq.h."""
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+    if not isinstance(k, _Tensor) or k.dim() != 3:
         raise ValueError("k must be [rows, heads, D]")
-    rows, _, D = k.shape
-    c = _kv(cache, table, lens, D, G, bits)
-    dev = cache.device
-    _need_rows(k, "k", dev, (rows, c.heads, D))
-    _need_rows(v, "v", dev, (rows, c.heads, D))
+    shape = k.shape
+    rows, heads, D = shape
+    c, dev = _kv(cache, table, lens, D, G, bits)
+    if heads != c.heads:
+        raise ValueError(f"k must have the cache's {c.heads} heads")
+    _need_rows(k, "k", dev, shape)
+    _need_rows(v, "v", dev, shape)
     off = _need_offsets(offsets, dev, c.batch, rows)
     if rows == 0:
         return
-    with _on(dev):
-        rc = lib().aq_kv_append(c, k.data_ptr(), _step(k, 0), _step(k, 1), v.data_ptr(), _step(v, 0), _step(v, 1),
-                                rows, off, _stream(cache))
-    _check(rc, "aq_kv_append")
+    ks, vs = _steps(k), _steps(v)
+    _call((_lib or lib()).aq_kv_append, "aq_kv_append", dev, c, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+          rows, off)
 
 
 def aq_kv_read(cache, table, lens, rows: int, D: int, G: int, bits: int, offsets: torch.Tensor | None = None, out=None):
     """-> (k, v), bf16 [rows, heads, D]: what the cache holds for the last tokens of each sequence, laid out by
     offsets as in aq_kv_append.  out: a (k, v) to write into; rows of no sequence stay as they are there."""
-    c = _kv(cache, table, lens, D, G, bits)
-    dev = cache.device
+    c, dev = _kv(cache, table, lens, D, G, bits)
     off = _need_offsets(offsets, dev, c.batch, rows)
     shape = (rows, c.heads, D)
     if out is None:
-        out = (torch.empty(shape, dtype=torch.bfloat16, device=dev), torch.empty(shape, dtype=torch.bfloat16, device=dev))
+        k = torch.empty(shape, dtype=_BF16, device=cache.device)
+        out = (k, torch.empty_like(k))
     else:
-        for t, name in zip(out, ("k of out", "v of out"), strict=True):
-            _need(t, name, (torch.bfloat16,), 3)
+        k, v = out
+        for t, name in ((k, "k of out"), (v, "v of out")):
+            _need(t, name, (_BF16,), 3)
             _need_rows(t, name, dev, shape)
     if rows == 0:
         return out
-    with _on(dev):
-        rc = lib().aq_kv_read(c, rows, off, out[0].data_ptr(), out[1].data_ptr(), _stream(cache))
-    _check(rc, "aq_kv_read")
+    _call((_lib or lib()).aq_kv_read, "aq_kv_read", dev, c, rows, off, out[0].data_ptr(), out[1].data_ptr())
     return out
 
 
 def aq_kv_attention_workspace_bytes(cache, table, lens, tokens: int, q_heads: int, D: int, G: int, bits: int,
                                     window: int = 0) -> int:
-    return int(lib().aq_kv_attention_workspace_bytes(_kv(cache, table, lens, D, G, bits), tokens, q_heads, window))
+    return int(lib().aq_kv_attention_workspace_bytes(_kv(cache, table, lens, D, G, bits)[0], tokens, q_heads, window))
 
 
 def aq_kv_attention(q, cache, table, lens, G: int, bits: int, scale: float | None = None, window: int = 0,
@@ -726,37 +747,37 @@ def aq_kv_attention(q, cache, table, lens, G: int, bits: int, scale: float | Non
     window: positions a token sees, itself included (0: all); lse fp32 [batch, tokens, q_heads]: written if given;
     workspace: a CUDA tensor of at least aq_kv_attention_workspace_bytes(...) bytes (None: allocated for the call).
     See aq_kv_attention in include/aq.h."""
-    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+    if not isinstance(q, _Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be [batch, tokens, q_heads, D] or [batch, q_heads, D]")
     shape = q.shape
     D, q_heads = shape[-1], shape[-2]
-    tokens = shape[1] if q.dim() == 4 else 1
-    c = _kv(cache, table, lens, D, G, bits)
-    dev = cache.device
-    _need_rows(q, "q", dev, (c.batch, *shape[1:]))
+    tokens = shape[1] if len(shape) == 4 else 1
+    c, dev = _kv(cache, table, lens, D, G, bits)
+    batch = c.batch
+    if shape[0] != batch:
+        raise ValueError(f"q must have a row for each of {batch} sequences")
+    _need_rows(q, "q", dev, shape)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
-        _need(out, "out", (torch.bfloat16,), q.dim())
+        _need(out, "out", (_BF16,), len(shape))
         _need_rows(out, "out", dev, shape)
     lp = 0
     if lse is not None:
-        _need(lse, "lse", (torch.float32,), q.dim() - 1)
-        if lse.device != dev or lse.shape != shape[:-1]:
+        _need(lse, "lse", (torch.float32,), len(shape) - 1)
+        if lse.get_device() != dev or lse.shape != shape[:-1]:
             raise ValueError(f"lse must be {list(shape[:-1])} on the cache's device")
         lp = lse.data_ptr()
-    if c.batch == 0:
+    if batch == 0:
         return out
-    L = lib()
-    need = L.aq_kv_attention_workspace_bytes(c, tokens, q_heads, window)
+    L = _lib or lib()
     if workspace is None:
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
+        # (0 for sizes that the call will refuse)
+        workspace = cache.new_empty((L.aq_kv_attention_workspace_bytes(c, tokens, q_heads, window),))
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    wp, wb = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    with _on(dev):
-        rc = L.aq_kv_attention(c, q.data_ptr(), tokens, q_heads, _step(q, 0), _step(q, 1) if q.dim() == 4 else 0,
-                               _step(q, -2), D**-0.5 if scale is None else scale, window, out.data_ptr(), lp, wp, wb, _stream(cache))
-    _check(rc, "aq_kv_attention")
+    st = _steps(q)
+    _call(L.aq_kv_attention, "aq_kv_attention", dev, c, q.data_ptr(), tokens, q_heads, st[0],
+          st[1] if len(st) == 4 else 0, st[-2], D**-0.5 if scale is None else scale, window, out.data_ptr(), lp,
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
