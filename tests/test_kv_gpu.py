@@ -238,6 +238,30 @@ def test_attention_window_far_from_the_start():
     _attend(c, queries(2, 2, 2, 64, 44), window=200)
 
 
+@pytest.mark.parametrize("bits", (4, 8))
+@pytest.mark.parametrize("bad", (0x7C00, 0xFC00, 0x7E01))
+def test_attention_beside_tokens_that_are_not_finite(bits, bad):
+    """A drafted token whose scales and biases are infinite or NaN, and one in front of the window: rows that do not see
+    them are as they would be without."""
+    D, G, n, window = 64, 32, 4, 25
+    c = filled([60, 35], heads=1, page_size=16, D=D, G=G, bits=bits, seed=45)
+    q = queries(2, n, 6, D, 46)
+    good = on_gpu(c)
+    r = ref.attention(c, q, 0.125, window)
+    for b, length in enumerate(c.lens.tolist()):
+        # the last token is seen by the last row alone; the one at length - n + 1 - window + 1 by rows 0 and 1 alone
+        for pos in (length - 1, length - n + 2 - window):
+            page, tile, row = c.locate(b, pos)
+            flat = c.data[page, 0].reshape(-1)
+            for which in (0, 1):
+                flat[c.spans(tile, row, which)[1]] = np.full(2 * c.ng, bad, np.uint16).view(np.uint8)
+    data, table, ln = on_gpu(c)
+    for gpu, rows_ok in (((data, table, ln), [2]), (good, [0, 1, 2, 3])):
+        x = aq.aq_kv_attention(to_gpu(q), *gpu, G, bits, scale=0.125, window=window).float().cpu().numpy().astype(np.float64)
+        far, _ = ref.attention_bounds(r, D)
+        assert (np.abs(x - r["out"]) <= far)[:, rows_ok].all()
+
+
 @pytest.mark.parametrize("scale", (0.0, -0.125, 3.0, 1e-6))
 def test_attention_scales(scale):
     c = filled([77, 30], heads=2, page_size=16, D=64, G=32, bits=8, seed=51)

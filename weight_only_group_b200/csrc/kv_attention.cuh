@@ -86,18 +86,27 @@ struct Plan {
   Loose *loose;      // [ctas]
 };
 
+// Positions in 32 bits: the table holds at most 2^30 of them (cap), lengths below 0 count as 0, and a window's begin is
+// taken as max(p + 1, window) - window, which neither a far negative p nor a large window can wrap.
+AQ_DEVICE int cap_of(const AttentionArgs &a) { return a.c.width << a.c.page_shift; }
+AQ_DEVICE int end_of(const AttentionArgs &a, int p) { return max(0, min(p + 1, cap_of(a))); }  // behind what position p sees
+AQ_DEVICE int begin_of(const AttentionArgs &a, int p) {
+  return a.window ? min(end_of(a, p), max(p + 1, a.window) - a.window) : 0;
+}
+
 // Positions that a sequence's new tokens see between them, as chunks.
 struct Span {
-  int len, begin, first, chunks;  // length and first position; first chunk; at least one, so that rows that see nothing are written too
+  int len, begin;     // length and first position
+  int first, chunks;  // first chunk; at least one, so that rows that see nothing are written too
 };
 template <int CHUNK>
 AQ_DEVICE Span span_of(const AttentionArgs &a, int seq) {
-  const int len32 = __ldg(a.c.lens + seq);
-  const int64_t len = len32, cap = int64_t(a.c.width) << a.c.page_shift;
-  const int64_t end = max(int64_t(0), min(len, cap));
-  const int64_t lo = a.window ? max(int64_t(0), min(end, len - a.tokens + 1 - a.window)) : 0;
-  const int first = static_cast<int>(lo / CHUNK);
-  return Span{len32, static_cast<int>(lo), first, max(1, static_cast<int>((end + CHUNK - 1) / CHUNK) - first)};
+  Span x;
+  x.len = max(0, __ldg(a.c.lens + seq));
+  x.begin = begin_of(a, x.len - a.tokens);
+  x.first = x.begin / CHUNK;
+  x.chunks = max(1, (min(x.len, cap_of(a)) + CHUNK - 1) / CHUNK - x.first);
+  return x;
 }
 
 AQ_DEVICE void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -213,76 +222,67 @@ AQ_DEVICE void prefetch_queries(const AttentionArgs &a, int seq, int h, int row0
 }
 
 template <int BITS, int D, int G, int NT>
-AQ_DEVICE void start_unit(State<BITS, D, G, NT> &st, const Queries<BITS, D, G, NT> &in, const AttentionArgs &a,
-                          int64_t len, int row0) {
+AQ_DEVICE void start_unit(State<BITS, D, G, NT> &st, const Queries<BITS, D, G, NT> &in, const AttentionArgs &a, int len,
+                          int row0) {
   using F = Form<BITS, D, G, NT>;
   using Q = Queries<BITS, D, G, NT>;
   constexpr int KW = Q::kKW, PW = Q::kPW;
   const int t = threadIdx.x & 3;
-  const int64_t cap = int64_t(a.c.width) << a.c.page_shift;
-  // the positions that the unit's first and last rows, and with them all of its rows, stand at
-  auto position = [&](int r) { return len - a.tokens + (a.tokens == 1 ? 0 : min(r, a.tokens * a.group - 1) / a.group); };
-  auto end_of = [&](int64_t p) { return static_cast<int>(max(int64_t(0), min(p + 1, cap))); };
-  auto begin_of = [&](int64_t p) {
-    return a.window ? static_cast<int>(max(int64_t(0), min(int64_t(end_of(p)), p + 1 - a.window))) : 0;
-  };
-  st.hi_all = end_of(position(row0));
-  st.lo_all = begin_of(position(row0 + F::kRows - 1));
+  const int rows = a.tokens * a.group;
+  auto position = [&](int r) { return len - a.tokens + (a.tokens == 1 ? 0 : min(r, rows - 1) / a.group); };
+  st.hi_all = end_of(a, position(row0));
+  st.lo_all = begin_of(a, position(row0 + F::kRows - 1));
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    uint32_t top = 0;
+    __nv_bfloat162 big = __bfloat162bfloat162(__ushort_as_bfloat16(0));
 #pragma unroll
     for (int gi = 0; gi < F::kNG; ++gi)
 #pragma unroll
       for (int w = 0; w < KW; ++w)
 #pragma unroll
-        for (int k = 0; k < PW / 2; ++k) {
-          const uint32_t v = in.raw[nt][gi][w][k];
-          top = max(top, max(v & 0x7FFFu, (v >> 16) & 0x7FFFu));
-        }
+        for (int k = 0; k < PW / 2; ++k)
+          big = __hmax2(big, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&in.raw[nt][gi][w][k])));
+    uint32_t top = max(__bfloat16_as_ushort(__low2bfloat16(big)), __bfloat16_as_ushort(__high2bfloat16(big)));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     // 2^e puts the row's largest |q| in [2^14, 2^15): bf16's 8 bits are exact in fp16 down to 2^-28 of it
     const int e = min(120, max(-100, 141 - static_cast<int>(top >> 7)));
-    const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
-    float qsum[F::kNG];
+    const float up = __uint_as_float((static_cast<uint32_t>(e + 127) << 23) | (__float_as_uint(a.scale) & 0x80000000u));
+    const float up4 = BITS == 4 ? up * 0.0625f : up;
 #pragma unroll
     for (int gi = 0; gi < F::kNG; ++gi) {
-      float sum = 0.0f;
+      float sum[4];
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
         float x[PW];
 #pragma unroll
-        for (int k = 0; k < PW / 2; ++k) {
-          x[2 * k] = __uint_as_float(in.raw[nt][gi][w][k] << 16) * up;
-          x[2 * k + 1] = __uint_as_float(in.raw[nt][gi][w][k] & 0xFFFF0000u) * up;
+        for (int k = 0; k < PW / 2; ++k) {  // (value k of the word, in the order in which unpack_k gives its codes)
+          x[2 * k] = __uint_as_float(in.raw[nt][gi][w][k] << 16);
+          x[2 * k + 1] = __uint_as_float(in.raw[nt][gi][w][k] & 0xFFFF0000u);
         }
-        // the order in which unpack_k gives a word's codes
-        constexpr float up4 = BITS == 4 ? 0.0625f : 1.0f;
 #pragma unroll
         for (int s = 0; s < PW / 4; ++s) {
           const int k = (gi * KW + w) * (PW / 4) + s;
           const int o = BITS == 4 ? 2 * s : 0, n = BITS == 4 ? 4 : 2;
-          st.q[nt][k][0] = pack_half2(x[o], x[o + n]);
+          st.q[nt][k][0] = pack_half2(x[o] * up, x[o + n] * up);
           st.q[nt][k][1] = pack_half2(x[o + 1] * up4, x[o + 1 + n] * up4);
-          const float2 f0 = pair_of(st.q[nt][k][0]), f1 = pair_of(st.q[nt][k][1]);
-          sum += f0.x + f0.y + (f1.x + f1.y) * (1.0f / up4);
+          // the sum over the group, of what the products will see: a product with ones (16 where q is a 16th)
+          constexpr uint32_t ONE = 0x3C003C00u, UP = BITS == 4 ? 0x4C004C00u : ONE;
+          if (w == 0 && s == 0) mma16816_first(sum, ONE, ONE, UP, UP, st.q[nt][k][0], st.q[nt][k][1]);
+          else mma16816(sum, ONE, ONE, UP, UP, st.q[nt][k][0], st.q[nt][k][1]);
         }
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      qsum[gi] = sum * 0x1p-24f;
+      st.qsum[nt][gi][0] = sum[0] * 0x1p-24f;
+      st.qsum[nt][gi][1] = sum[1] * 0x1p-24f;
     }
-    const float rs = ldexpf(fabsf(a.scale) * CUDART_L2E_F, 24 - e);
+    // (a scale of 0 as the smallest there is, so that what is not seen keeps its -infinity)
+    const float rs = fmaxf(ldexpf(fabsf(a.scale) * CUDART_L2E_F, 24 - e), 0x1p-126f);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int src = (2 * t + c) * 4;
-#pragma unroll
-      for (int gi = 0; gi < F::kNG; ++gi) st.qsum[nt][gi][c] = __shfl_sync(0xffffffffu, qsum[gi], src);
-      st.rs[nt][c] = __shfl_sync(0xffffffffu, rs, src);
-      const int64_t p = position(row0 + nt * 8 + 2 * t + c);
-      st.hi[nt][c] = end_of(p);
-      st.lo[nt][c] = begin_of(p);
+      st.rs[nt][c] = __shfl_sync(0xffffffffu, rs, (2 * t + c) * 4);
+      const int p = position(row0 + nt * 8 + 2 * t + c);
+      st.hi[nt][c] = end_of(a, p);
+      st.lo[nt][c] = begin_of(a, p);
       st.m[nt][c] = -1e30f;
       st.l[nt][c] = 0.0f;
 #pragma unroll
@@ -311,8 +311,8 @@ AQ_DEVICE void unpack_k(uint32_t w, uint32_t (&x)[16 / BITS]) {
 }
 
 // One chunk: kCT tiles in shared memory, the first of them at position pos.
-// valid: bit i, tile i was copied.  WHOLE: every row sees every token.
-template <bool WHOLE, int BITS, int D, int G, int NT>
+// valid: bit i, tile i was copied.
+template <int BITS, int D, int G, int NT>
 AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int pos, uint32_t valid) {
   using F = Form<BITS, D, G, NT>;
   constexpr int KW = F::kGroupBytes / 16;
@@ -375,15 +375,18 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
       }
     }
   }
-  // --- which tokens a row sees; what no row sees may be anything, so its scales and biases are not used
-  uint32_t seen = 0xFFFFFFFFu;  // bit (i * NT + nt) * 4 + c
-  if constexpr (!WHOLE) {
-    seen = 0;
+  // --- which tokens a row sees.  What it does not see weighs 2^-infinity = 0, and where a scale or bias might be infinite
+  // or NaN the products are zeroed too: it is where no row sees the token (nothing may have been written there), and it may
+  // be where another row does (seen: bit (i * NT + nt) * 4 + c; partly: some row sees a token that another does not)
+  uint32_t seen = 0;
+  bool partly = false;
+  if (valid != (1u << CT) - 1u || pos < st.lo_all || pos + kTile * CT > st.hi_all) {
 #pragma unroll
-    for (int i = 0; i < CT; ++i) {
+    for (int i = 0; i < CT; ++i)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int at = pos + i * kTile + half * 8 + tok;
+        bool any = false, all = true;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -391,25 +394,18 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
             const bool see = (valid >> i & 1) && at >= st.lo[nt][c] && at < st.hi[nt][c];
             if (see) seen |= 1u << ((i * NT + nt) * 4 + half * 2 + c);
             else x[i][nt][half * 2 + c] = -CUDART_INF_F;
+            any |= see;
+            all &= see;
           }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < CT; ++i) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t mine = 0;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mine |= seen >> ((i * NT + nt) * 4 + half * 2) & 3u;
-        // the four lanes of a token hold different rows: what any of them sees counts
-        mine |= __shfl_xor_sync(0xffffffffu, mine, 1);
-        mine |= __shfl_xor_sync(0xffffffffu, mine, 2);
-        if (!mine) {
+        // (the four lanes of a token hold different rows: what any of them sees counts)
+        any = __ballot_sync(0xffffffffu, any) >> (lane & 28) & 15u;
+        partly |= any && !all;
+        if (!any) {
 #pragma unroll
           for (int gi = 0; gi < NG; ++gi) sv[i][half][gi] = 0;
         }
       }
-    }
+    partly = __any_sync(0xffffffffu, partly);
   }
   // --- the running reference.  A weight is 2^(x - m): m is the row's maximum so far + e - 15, where every V scale so far is
   // below 2^e, so that (weight * scale) stays below 2^15 and is a normal fp16 down to 2^-29 of that: what rounds to nothing
@@ -465,10 +461,8 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        float p = exp2_approx(fmaf(x[i][nt][c], st.rs[nt][c & 1], -st.m[nt][c & 1]));
-        if (!WHOLE && !(seen >> ((i * NT + nt) * 4 + c) & 1)) p = 0.0f;
-        x[i][nt][c] = p;
-        st.l[nt][c & 1] += p;
+        x[i][nt][c] = exp2_approx(fmaf(x[i][nt][c], st.rs[nt][c & 1], -st.m[nt][c & 1]));
+        st.l[nt][c & 1] += x[i][nt][c];
       }
     const uint8_t *v = stage + i * F::kTileBytes + kTile * F::kRow + t * F::kRow + g * (F::kGroupBytes / 8);
 #pragma unroll
@@ -477,16 +471,20 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
       uint32_t b[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float y[4];
+        float y[4], z[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float2 sb = c < 2 ? p0 : p1;
           y[c] = x[i][nt][c] * sb.x;
-          float z = x[i][nt][c] * sb.y;
-          // (a scale or bias that this row does not see may be infinite or NaN where another row's token is)
-          if (!WHOLE && !(seen >> ((i * NT + nt) * 4 + c) & 1)) y[c] = z = 0.0f;
-          st.bias[nt][gi][c & 1] += z;
+          z[c] = x[i][nt][c] * sb.y;
         }
+        if (partly) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (!(seen >> ((i * NT + nt) * 4 + c) & 1)) y[c] = z[c] = 0.0f;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) st.bias[nt][gi][c] += z[c] + z[2 + c];
         b[nt][0] = transpose8x8(pack_half2(y[0], y[1]));
         b[nt][1] = transpose8x8(pack_half2(y[2], y[3]));
       }
@@ -619,27 +617,25 @@ AQ_DEVICE void write_part(const State<BITS, D, G, NT> &st, float *part) {
     }
 }
 
-// Joins n <= MAX partial results, part(0) .. part(n - 1) in this order: calls put(row, column / 4, sum, reference,
-// weights' sum) for every four columns.  All threads of the CTA.
-template <int ROWS, int D, int MAX, class Part, class Put>
+// Joins n partial results, part(0) .. part(n - 1) in this order: calls put(row, column / 4, sum, reference, weights'
+// sum) for every four columns.  All threads of the CTA.  (Run once, so its loops stay loops: instructions that are new to
+// an SM cost more than their steps.)
+template <int ROWS, int D, class Part, class Put>
 AQ_DEVICE void join(int n, Part part, Put put) {
+#pragma unroll 1
   for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
     const int r = i / (D / 4), c = i - r * (D / 4);
-    float mk[MAX], m = -1e30f, l = 0.0f;
-#pragma unroll
-    for (int k = 0; k < MAX; ++k) mk[k] = k < n ? part(k)[r] : -1e30f;
-#pragma unroll
-    for (int k = 0; k < MAX; ++k) m = fmaxf(m, mk[k]);
+    float m = -1e30f, l = 0.0f;
+#pragma unroll 2
+    for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[r]);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int k = 0; k < MAX; ++k) {
-      if (k < n) {
-        const float *p = part(k);
-        const float w = exp2_approx(mk[k] - m);
-        const float4 v = reinterpret_cast<const float4 *>(p + 2 * ROWS)[i];
-        l = fmaf(w, p[ROWS + r], l);
-        o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
-      }
+#pragma unroll 2
+    for (int k = 0; k < n; ++k) {
+      const float *p = part(k);
+      const float w = exp2_approx(p[r] - m);
+      const float4 v = reinterpret_cast<const float4 *>(p + 2 * ROWS)[i];
+      l = fmaf(w, p[ROWS + r], l);
+      o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
     }
     put(r, c, o, m, l);
   }
@@ -818,13 +814,10 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
         ok = mbar_wait(&bars[warp][stage], parity, &abort_flag, &g_fault, kFaultQmvWait);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        --flying;
-        const uint8_t *tiles = ring + stage * F::kStage;
-        const uint32_t valid = valid_bits & ((1u << CT) - 1u);
-        valid_bits >>= CT;
-        if (valid == (1u << CT) - 1u && pos >= st.lo_all && pos + CHUNK <= st.hi_all) run_chunk<true>(st, tiles, pos, valid);
-        else run_chunk<false>(st, tiles, pos, valid);
+        run_chunk(st, ring + stage * F::kStage, pos, valid_bits & ((1u << CT) - 1u));
         __syncwarp();
+        --flying;
+        valid_bits >>= CT;
         if (left > 0) issue();
         if (++stage == F::kStages) stage = 0, parity ^= 1;
       }
@@ -832,20 +825,22 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
       at += take;  // the place behind this unit's part, or behind the unit
       finish_unit(st);
       const int id = cur.seq * units + cur.head * plan.row_tiles + cur.row_tile;
-      if (first == 0 && take == cur.span.chunks) {
+      const bool whole = take == cur.span.chunks, ends = first + take == cur.span.chunks;
+      if (whole) {
         write_out(st, a, cur.seq, cur.head, row0);
-      } else if (first + take == cur.span.chunks) {
-        write_part(st, plan.heads + (int64_t(blockIdx.x) * kWarps + warp) * F::kPart);
-        if (lane == 0) head_unit[warp] = id;
-      } else {  // the warp's last: its ring is free
-        write_part(st, reinterpret_cast<float *>(ring));
+      } else {  // a part: the end of a unit that another warp began, or the warp's last, when its ring is free
+        write_part(st, ends ? plan.heads + (int64_t(blockIdx.x) * kWarps + warp) * F::kPart : reinterpret_cast<float *>(ring));
         if (lane == 0) {
-          tail_unit[warp] = id;
-          tail_end[warp] = at - first - take + cur.span.chunks;  // the place behind the unit
-          tail_starts[warp] = first == 0;
+          if (ends) {
+            head_unit[warp] = id;
+          } else {
+            tail_unit[warp] = id;
+            tail_end[warp] = at - first - take + cur.span.chunks;  // the place behind the unit
+            tail_starts[warp] = first == 0;
+          }
         }
       }
-      if (cur.span.len > (int64_t(a.c.width) << a.c.page_shift) && lane == 0) atomicOr(&g_fault, kFaultBadIndex);
+      if (cur.span.len > cap_of(a) && lane == 0) atomicOr(&g_fault, kFaultBadIndex);
       at += kUnitCost;  // the next unit's first chunk
       if (at >= end) break;
       cur.next_unit(a, plan.row_tiles);
@@ -879,20 +874,17 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
       auto part = [&](int k) -> const float * {
         return ends && k == n - 1 ? end_part : reinterpret_cast<const float *>(smem + ((first >> 1) + k) * F::kRing);
       };
-      if (starts && ends) {
-        const int seq = id / units, u = id - seq * units, h = u / plan.row_tiles;
-        const int row0 = (u - h * plan.row_tiles) * F::kRows;
-        join<F::kRows, D, kWarps>(n, part, [&](int r, int c, float4 o, float m, float l) {
+      const int seq = id / units, u = id - seq * units, h = u / plan.row_tiles, row0 = (u - h * plan.row_tiles) * F::kRows;
+      float *dst = plan.parts + (int64_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * F::kPart;
+      join<F::kRows, D>(n, part, [&](int r, int c, float4 o, float m, float l) {
+        if (starts && ends) {
           put_out<D>(a, seq, h, row0 + r, c, o, m, l);
-        });
-      } else {
-        float *dst = plan.parts + (int64_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * F::kPart;
-        join<F::kRows, D, kWarps>(n, part, [&](int r, int c, float4 o, float m, float l) {
+        } else {
           if (c == 0) dst[r] = m, dst[F::kRows + r] = l;
           reinterpret_cast<float4 *>(dst + 2 * F::kRows)[r * (D / 4) + c] = o;
-        });
-        if (starts) loose = Loose{id, (tail_end[first >> 1] - 1) / (kWarps * share)};
-      }
+        }
+      });
+      if (starts && !ends) loose = Loose{id, (tail_end[first >> 1] - 1) / (kWarps * share)};
     }
   }
   if (threadIdx.x == 0 && !plan.direct) plan.loose[blockIdx.x] = loose;
