@@ -263,9 +263,13 @@ AQ_DEVICE void start_unit(State<BITS, D, G, NT> &st, const Queries<BITS, D, G, N
 #pragma unroll
         for (int s = 0; s < PW / 4; ++s) {
           const int k = (gi * KW + w) * (PW / 4) + s;
-          const int o = BITS == 4 ? 2 * s : 0, n = BITS == 4 ? 4 : 2;
-          st.q[nt][k][0] = pack_half2(x[o] * up, x[o + n] * up);
-          st.q[nt][k][1] = pack_half2(x[o + 1] * up4, x[o + 1 + n] * up4);
+          if constexpr (BITS == 4) {
+            st.q[nt][k][0] = pack_half2(x[2 * s] * up, x[2 * s + 4] * up);
+            st.q[nt][k][1] = pack_half2(x[2 * s + 1] * up4, x[2 * s + 5] * up4);
+          } else {
+            st.q[nt][k][0] = pack_half2(x[0] * up, x[1] * up);
+            st.q[nt][k][1] = pack_half2(x[2] * up, x[3] * up);
+          }
           // the sum over the group, of what the products will see: a product with ones (16 where q is a 16th)
           constexpr uint32_t ONE = 0x3C003C00u, UP = BITS == 4 ? 0x4C004C00u : ONE;
           if (w == 0 && s == 0) mma16816_first(sum, ONE, ONE, UP, UP, st.q[nt][k][0], st.q[nt][k][1]);
@@ -305,8 +309,8 @@ AQ_DEVICE void unpack_k(uint32_t w, uint32_t (&x)[16 / BITS]) {
     x[2] = (w >> 8) & 0x000F000Fu;
     x[3] = (w >> 8) & 0x00F000F0u;
   } else {
-    x[0] = w & 0x00FF00FFu;  // codes 0, 2
-    x[1] = (w >> 8) & 0x00FF00FFu;
+    x[0] = __byte_perm(w, 0u, 0x4140u);  // codes 0, 1
+    x[1] = __byte_perm(w, 0u, 0x4342u);  // codes 2, 3
   }
 }
 
@@ -407,9 +411,10 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
       }
     partly = __any_sync(0xffffffffu, partly);
   }
-  // --- the running reference.  A weight is 2^(x - m): m is the row's maximum so far + e - 15, where every V scale so far is
-  // below 2^e, so that (weight * scale) stays below 2^15 and is a normal fp16 down to 2^-29 of that: what rounds to nothing
-  // is smaller than a 2^-39th of the largest
+  // --- the running reference m of a row.  A weight is 2^(x - m), m = (a maximum so far) + e - 11, where V scales so far are
+  // below 2^e.  m stands while no weight times scale can pass 2^15: scores at most 2^4 above the maximum it was taken from,
+  // scales below 2^e.  So a look at this lane's own values is enough but for the first chunks and the rare new extreme.
+  // (weight * scale) is a normal fp16 down to 2^-25 of the largest, and rounds to nothing below a 2^-36th of it.
   __half2 top = __half2half2(__ushort_as_half(0));  // (scale, bias): the low half is what counts; a NaN is passed over
 #pragma unroll
   for (int i = 0; i < CT; ++i)
@@ -418,9 +423,8 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
 #pragma unroll
       for (int gi = 0; gi < NG; ++gi) top = __hmax2(top, *reinterpret_cast<const __half2 *>(&sv[i][half][gi]));
   const uint32_t top_bits = __half_as_ushort(__low2half(top));
-  const int e = max(st.e, static_cast<int>(__reduce_max_sync(0xffffffffu, top_bits) >> 10) - 14);
   float mx[NT][2];
-  bool more = e > st.e;
+  bool more = static_cast<int>(top_bits >> 10) - 14 > st.e;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -428,20 +432,22 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
       float v = fmaxf(x[0][nt][c], x[0][nt][2 + c]);
 #pragma unroll
       for (int i = 1; i < CT; ++i) v = fmaxf(v, fmaxf(x[i][nt][c], x[i][nt][2 + c]));
-      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-      mx[nt][c] = fmaf(v, st.rs[nt][c], static_cast<float>(e - 15));
-      more |= mx[nt][c] > st.m[nt][c];
+      mx[nt][c] = v;
+      more |= fmaf(v, st.rs[nt][c], static_cast<float>(st.e - 15)) > st.m[nt][c];
     }
   if (__any_sync(0xffffffffu, more)) {
+    const int e = max(st.e, static_cast<int>(__reduce_max_sync(0xffffffffu, top_bits) >> 10) - 14);
     const float shift = static_cast<float>(e - st.e);
     st.e = e;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float mn = fmaxf(st.m[nt][c] + shift, mx[nt][c]);
+        float v = mx[nt][c];
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        const float mn = fmaxf(st.m[nt][c] + shift, fmaf(v, st.rs[nt][c], static_cast<float>(e - 11)));
         const float al = exp2_approx(st.m[nt][c] - mn);
         st.m[nt][c] = mn;
         st.l[nt][c] *= al;
@@ -732,12 +738,10 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
     const int to = static_cast<int>(min(int64_t(total), int64_t(from) + share));
     begin = end = 0;
     if (from < to) {
-      int lo = 0, hi = kThreads;  // the last share of sequences that begins at or before the run
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sums[mid] * units <= from) lo = mid;
-        else hi = mid;
-      }
+      // the last share of sequences that begins at or before the run
+      int lo = 31 - __clz(__ballot_sync(0xffffffffu, sums[lane * (kThreads / 32)] * units <= from));
+      lo = lo * (kThreads / 32) + 31 -
+           __clz(__ballot_sync(0xffffffffu, lane < kThreads / 32 && sums[lo * (kThreads / 32) + lane] * units <= from));
       int at = sums[lo] * units;
       cur.seq = lo * per;
       cur.span = span_of<CHUNK>(a, cur.seq);
