@@ -50,22 +50,31 @@ constexpr int kSms = 148;  // the grid never has more CTAs than these hold
 // Units of at most so many chunks, and no more of them than CTAs, get a CTA each: no list of places, no second kernel.
 constexpr int kDirectChunks = 2 * kWarps;
 
-template <int BITS, int D, int G, int NT>
+// ROWS: query rows that a unit takes, 4, 8 or 16.
+template <int BITS, int D, int G, int ROWS>
 struct Form {
   static constexpr int kNG = D / G;                  // groups of a row
   static constexpr int kRow = D * BITS / 8;          // bytes of a row of codes
   static constexpr int kGroupBytes = G * BITS / 8;
   static constexpr int kMeta = meta_bytes(D, G);     // bytes of a token's pairs
   static constexpr int kTileBytes = tile_bytes(D, G, BITS);
-  // Tiles of a chunk: two share the maximum's shuffles; one where a ring of
+  // Columns of the matrix instructions: see State.
+  static constexpr bool kPair = ROWS == 4;
+  static constexpr int kNT = ROWS == 16 ? 2 : 1, kRL = kPair ? 1 : 2;
+  static __host__ __device__ constexpr int col(int gi, int c) { return kPair ? gi & 1 : c; }
+  static __host__ __device__ constexpr int row_of(int nt, int t, int c) { return kPair ? t : nt * 8 + 2 * t + c; }
+  // Groups whose products share an accumulator: gi is the first of them, the last, and which is the first.
+  static __host__ __device__ constexpr bool first_of(int gi) { return !kPair || (gi & 1) == 0; }
+  static __host__ __device__ constexpr bool last_of(int gi) { return !kPair || (gi & 1) == 1 || gi == kNG - 1; }
+  static __host__ __device__ constexpr int begin_of(int gi) { return kPair ? gi & ~1 : gi; }
+  // Tiles of a chunk: two share a look at the maximum; one where a ring of
   // two-tile stages would leave no room for three stages.
   static constexpr int kCT = kTileBytes > 4800 ? 1 : 2;
   static constexpr int kStage = kCT * kTileBytes;
-  static constexpr int kRows = 8 * NT;               // query rows of a unit
-  static constexpr int kPart = kRows * (D + 2);      // floats of a partial result: max, sum, accumulator
+  static constexpr int kPart = ROWS * (D + 2);       // floats of a partial result: max, sum, accumulator
   // Two CTAs on an SM where their rings have two stages or more and 128 registers a thread hold the accumulator.
   static constexpr int kSmem = 224 * 1024;
-  static constexpr int kCtas = (NT == 1 && D <= 128 && kSmem / 2 / (kWarps * kStage) >= 2) ? 2 : 1;
+  static constexpr int kCtas = (ROWS <= 8 && D <= 128 && kSmem / 2 / (kWarps * kStage) >= 2) ? 2 : 1;
   static constexpr int kStages = kSmem / kCtas / (kWarps * kStage) > 4 ? 4 : kSmem / kCtas / (kWarps * kStage);
   static constexpr int kRing = kStages * kStage;     // bytes of a warp's ring
   static_assert(kStages >= 2 && kRing >= kPart * 4, "a warp's ring holds two stages, and its last partial result");
@@ -159,81 +168,90 @@ AQ_DEVICE void lds(uint32_t (&w)[N], const uint8_t *p) {
   }
 }
 
-// A running state of one warp over one unit: NT column tiles of query rows.  A
-// lane holds the rows 8 nt + 2 (lane % 4) + {0, 1}.
-template <int BITS, int D, int G, int NT>
+// A running state of one warp over one unit.  The matrix instructions have eight columns:
+//   16 rows: two sets of columns (NT = 2), a column for each row;
+//    8 rows: a column for each row;
+//    4 rows: a column for each row and each group of a pair of groups along d, so that the lanes that would hold rows
+//            that are not there hold half of the groups instead.
+// A lane holds columns 2 t and 2 t + 1 (t = lane % 4), which are RL rows: 8 nt + 2 t + {0, 1}, or row t.  Of a product whose
+// columns belong to groups, group gi's is column col(gi, c) of the lane's two.
+template <int BITS, int D, int G, int ROWS>
 struct State {
-  using F = Form<BITS, D, G, NT>;
+  using F = Form<BITS, D, G, ROWS>;
+  static constexpr int NT = F::kNT, RL = F::kRL;
   uint32_t q[NT][D / 16][2];     // q's fragments: fp16, times the row's power of two
-  float qsum[NT][F::kNG][2];     // sum of q over each group, times 2^-24
-  float rs[NT][2];               // a raw score times this is a score in powers of 2
-  int hi[NT][2], lo[NT][2];      // positions [lo, hi) are seen
-  int hi_all, lo_all;            // [lo_all, hi_all): seen by every row
-  float m[NT][2], l[NT][2];      // reference (the maximum, see below) and sum of weights, the latter of this lane's tokens
-  float bias[NT][F::kNG][2];     // sum of weights times V biases, of this lane's tokens
+  float qsum[NT][F::kNG][RL];    // sum of q over each group, times 2^-24
+  float rs[NT][RL];              // a raw score times this is a score in powers of 2
+  int pos[NT][RL];               // the row's position
+  int hi_all, lo_all;            // [lo_all, hi_all): positions seen by every row
+  float m[NT][RL], l[NT][RL];    // reference (see run_chunk) and sum of weights, the latter of this lane's tokens
+  float bias[NT][F::kNG][RL];    // sum of weights times V biases, of this lane's tokens
   float acc[NT][D / 16][4];      // sum of (weight * V scale) * code, times 2^-24
   int e;                         // V scales so far are below 2^e
 };
 
 // The query rows of a unit, as this lane's share of them: loaded early, looked at by start_unit.
-template <int BITS, int D, int G, int NT>
+template <int BITS, int D, int G, int ROWS>
 struct Queries {
   static constexpr int kKW = G * BITS / 128;  // words of a lane in a group of K: a quarter
   static constexpr int kPW = 32 / BITS;       // codes of a word
-  uint32_t raw[NT][D / G][kKW][kPW / 2];
+  uint32_t raw[Form<BITS, D, G, ROWS>::kNT][D / G][kKW][kPW / 2];
 };
 
-template <int BITS, int D, int G, int NT>
-AQ_DEVICE void load_queries(Queries<BITS, D, G, NT> &x, const AttentionArgs &a, int seq, int h, int row0) {
-  using Q = Queries<BITS, D, G, NT>;
+template <int BITS, int D, int G, int ROWS>
+AQ_DEVICE void load_queries(Queries<BITS, D, G, ROWS> &x, const AttentionArgs &a, int seq, int h, int row0) {
+  using F = Form<BITS, D, G, ROWS>;
+  using Q = Queries<BITS, D, G, ROWS>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = row0 + nt * 8 + g;
+  for (int nt = 0; nt < F::kNT; ++nt) {
+    const int r = row0 + nt * 8 + (F::kPair ? g >> 1 : g);  // the row of this lane's column g
     const bool real = r < a.tokens * a.group;
     const int j = a.tokens == 1 || !real ? 0 : r / a.group, i = real ? r - j * a.group : 0;
     const uint16_t *q = a.q + seq * a.q_stride[0] + j * a.q_stride[1] + (h * a.group + i) * a.q_stride[2];
 #pragma unroll
-    for (int gi = 0; gi < D / G; ++gi)
+    for (int gi = 0; gi < D / G; ++gi) {
+      const bool mine = real && (!F::kPair || (gi & 1) == (g & 1));
 #pragma unroll
       for (int w = 0; w < Q::kKW; ++w) {
         const uint16_t *p = q + gi * G + (t * Q::kKW + w) * Q::kPW;
         uint32_t(&v)[Q::kPW / 2] = x.raw[nt][gi][w];
         if constexpr (Q::kPW == 8) {
-          const uint4 u = real ? ldg_nc16(p) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 u = mine ? ldg_nc16(p) : make_uint4(0u, 0u, 0u, 0u);
           v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
         } else {
-          const uint2 u = real ? ldg_nc8(p) : make_uint2(0u, 0u);
+          const uint2 u = mine ? ldg_nc8(p) : make_uint2(0u, 0u);
           v[0] = u.x, v[1] = u.y;
         }
       }
+    }
   }
 }
 
 // Brings a unit's query rows near: a lane asks for one of their 128-byte lines.
-template <int D, int NT>
+template <int D, int ROWS>
 AQ_DEVICE void prefetch_queries(const AttentionArgs &a, int seq, int h, int row0) {
   constexpr int LINES = D / 64;
   const int lane = threadIdx.x & 31, r = row0 + lane / LINES;
-  if (lane >= 8 * NT * LINES || r >= a.tokens * a.group) return;
+  if (lane >= ROWS * LINES || r >= a.tokens * a.group) return;
   const int j = a.tokens == 1 ? 0 : r / a.group, i = r - j * a.group;
   const uint16_t *q = a.q + seq * a.q_stride[0] + j * a.q_stride[1] + (h * a.group + i) * a.q_stride[2];
   asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane % LINES * 64));
 }
 
-template <int BITS, int D, int G, int NT>
-AQ_DEVICE void start_unit(State<BITS, D, G, NT> &st, const Queries<BITS, D, G, NT> &in, const AttentionArgs &a, int len,
+template <int BITS, int D, int G, int ROWS>
+AQ_DEVICE void start_unit(State<BITS, D, G, ROWS> &st, const Queries<BITS, D, G, ROWS> &in, const AttentionArgs &a, int len,
                           int row0) {
-  using F = Form<BITS, D, G, NT>;
-  using Q = Queries<BITS, D, G, NT>;
-  constexpr int KW = Q::kKW, PW = Q::kPW;
+  using F = Form<BITS, D, G, ROWS>;
+  using Q = Queries<BITS, D, G, ROWS>;
+  constexpr int KW = Q::kKW, PW = Q::kPW, RL = F::kRL;
   const int t = threadIdx.x & 3;
   const int rows = a.tokens * a.group;
   auto position = [&](int r) { return len - a.tokens + (a.tokens == 1 ? 0 : min(r, rows - 1) / a.group); };
   st.hi_all = end_of(a, position(row0));
-  st.lo_all = begin_of(a, position(row0 + F::kRows - 1));
+  st.lo_all = begin_of(a, position(row0 + ROWS - 1));
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  for (int nt = 0; nt < F::kNT; ++nt) {
     __nv_bfloat162 big = __bfloat162bfloat162(__ushort_as_bfloat16(0));
 #pragma unroll
     for (int gi = 0; gi < F::kNG; ++gi)
@@ -245,23 +263,24 @@ AQ_DEVICE void start_unit(State<BITS, D, G, NT> &st, const Queries<BITS, D, G, N
     uint32_t top = max(__bfloat16_as_ushort(__low2bfloat16(big)), __bfloat16_as_ushort(__high2bfloat16(big)));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if (F::kPair) top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
     // 2^e puts the row's largest |q| in [2^14, 2^15): bf16's 8 bits are exact in fp16 down to 2^-28 of it
     const int e = min(120, max(-100, 141 - static_cast<int>(top >> 7)));
     const float up = __uint_as_float((static_cast<uint32_t>(e + 127) << 23) | (__float_as_uint(a.scale) & 0x80000000u));
     const float up4 = BITS == 4 ? up * 0.0625f : up;
+    float sum[4];
 #pragma unroll
     for (int gi = 0; gi < F::kNG; ++gi) {
-      float sum[4];
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
         float x[PW];
 #pragma unroll
-        for (int k = 0; k < PW / 2; ++k) {  // (value k of the word, in the order in which unpack_k gives its codes)
+        for (int k = 0; k < PW / 2; ++k) {
           x[2 * k] = __uint_as_float(in.raw[nt][gi][w][k] << 16);
           x[2 * k + 1] = __uint_as_float(in.raw[nt][gi][w][k] & 0xFFFF0000u);
         }
 #pragma unroll
-        for (int s = 0; s < PW / 4; ++s) {
+        for (int s = 0; s < PW / 4; ++s) {  // (in the order in which unpack_k gives a word's codes)
           const int k = (gi * KW + w) * (PW / 4) + s;
           if constexpr (BITS == 4) {
             st.q[nt][k][0] = pack_half2(x[2 * s] * up, x[2 * s + 4] * up);
@@ -272,21 +291,23 @@ AQ_DEVICE void start_unit(State<BITS, D, G, NT> &st, const Queries<BITS, D, G, N
           }
           // the sum over the group, of what the products will see: a product with ones (16 where q is a 16th)
           constexpr uint32_t ONE = 0x3C003C00u, UP = BITS == 4 ? 0x4C004C00u : ONE;
-          if (w == 0 && s == 0) mma16816_first(sum, ONE, ONE, UP, UP, st.q[nt][k][0], st.q[nt][k][1]);
+          if (w == 0 && s == 0 && F::first_of(gi)) mma16816_first(sum, ONE, ONE, UP, UP, st.q[nt][k][0], st.q[nt][k][1]);
           else mma16816(sum, ONE, ONE, UP, UP, st.q[nt][k][0], st.q[nt][k][1]);
         }
       }
-      st.qsum[nt][gi][0] = sum[0] * 0x1p-24f;
-      st.qsum[nt][gi][1] = sum[1] * 0x1p-24f;
+      if (F::last_of(gi)) {
+#pragma unroll
+        for (int gj = F::begin_of(gi); gj <= gi; ++gj)
+#pragma unroll
+          for (int c = 0; c < RL; ++c) st.qsum[nt][gj][c] = sum[F::col(gj, c)] * 0x1p-24f;
+      }
     }
     // (a scale of 0 as the smallest there is, so that what is not seen keeps its -infinity)
     const float rs = fmaxf(ldexpf(fabsf(a.scale) * CUDART_L2E_F, 24 - e), 0x1p-126f);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < RL; ++c) {
       st.rs[nt][c] = __shfl_sync(0xffffffffu, rs, (2 * t + c) * 4);
-      const int p = position(row0 + nt * 8 + 2 * t + c);
-      st.hi[nt][c] = end_of(a, p);
-      st.lo[nt][c] = begin_of(a, p);
+      st.pos[nt][c] = position(row0 + F::row_of(nt, t, c));
       st.m[nt][c] = -1e30f;
       st.l[nt][c] = 0.0f;
 #pragma unroll
@@ -316,16 +337,16 @@ AQ_DEVICE void unpack_k(uint32_t w, uint32_t (&x)[16 / BITS]) {
 
 // One chunk: kCT tiles in shared memory, the first of them at position pos.
 // valid: bit i, tile i was copied.
-template <int BITS, int D, int G, int NT>
-AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int pos, uint32_t valid) {
-  using F = Form<BITS, D, G, NT>;
+template <int BITS, int D, int G, int ROWS>
+AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, const uint8_t *stage, int pos, uint32_t valid) {
+  using F = Form<BITS, D, G, ROWS>;
   constexpr int KW = F::kGroupBytes / 16;
-  constexpr int CT = F::kCT, NG = F::kNG;
+  constexpr int CT = F::kCT, NG = F::kNG, NT = F::kNT, RL = F::kRL;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   // The token of matrix row r (and 8 + r): such that the tokens that V's fragments want in lane t are t, t + 4, t + 8 and
   // t + 12, neighbouring rows for neighbouring lanes.
   const int tok = ((g & 1) << 2) | (g >> 1);
-  float x[CT][NT][4];
+  float x[CT][NT][2][RL];  // raw scores, then weights: tokens tok and tok + 8 of each tile
   uint32_t sv[CT][2][NG];
   // --- scores
 #pragma unroll
@@ -341,16 +362,12 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
 #pragma unroll
       for (int gi = 0; gi < NG; ++gi) sk[half][gi] = kv[gi], sv[i][half][gi] = kv[NG + gi];
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) x[i][nt][c] = 0.0f;
+    float s[NT][4];
 #pragma unroll
     for (int gi = 0; gi < NG; ++gi) {
       uint32_t w0[KW], w1[KW];
       lds<KW>(w0, k0 + gi * F::kGroupBytes);
       lds<KW>(w1, k1 + gi * F::kGroupBytes);
-      float s[NT][4];
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
         uint32_t a0[16 / BITS], a1[16 / BITS];
@@ -361,27 +378,34 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
           const int k = (gi * KW + w) * (8 / BITS) + j;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if (w == 0 && j == 0)
+            if (w == 0 && j == 0 && F::first_of(gi))
               mma16816_first(s[nt], a0[0], a1[0], a0[1], a1[1], st.q[nt][k][0], st.q[nt][k][1]);
             else
               mma16816(s[nt], a0[2 * j], a1[2 * j], a0[2 * j + 1], a1[2 * j + 1], st.q[nt][k][0], st.q[nt][k][1]);
           }
         }
       }
-      const float2 p0 = pair_of(sk[0][gi]), p1 = pair_of(sk[1][gi]);
+      if (F::last_of(gi)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+        for (int gj = F::begin_of(gi); gj <= gi; ++gj)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          x[i][nt][c] = fmaf(p0.x, s[nt][c], fmaf(p0.y, st.qsum[nt][gi][c], x[i][nt][c]));
-          x[i][nt][2 + c] = fmaf(p1.x, s[nt][2 + c], fmaf(p1.y, st.qsum[nt][gi][c], x[i][nt][2 + c]));
-        }
+          for (int half = 0; half < 2; ++half) {
+            const float2 sb = pair_of(sk[half][gj]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < RL; ++c) {
+                const float b = gj == 0 ? sb.y * st.qsum[nt][gj][c] : fmaf(sb.y, st.qsum[nt][gj][c], x[i][nt][half][c]);
+                x[i][nt][half][c] = fmaf(sb.x, s[nt][half * 2 + F::col(gj, c)], b);
+              }
+          }
       }
     }
   }
   // --- which tokens a row sees.  What it does not see weighs 2^-infinity = 0, and where a scale or bias might be infinite
   // or NaN the products are zeroed too: it is where no row sees the token (nothing may have been written there), and it may
-  // be where another row does (seen: bit (i * NT + nt) * 4 + c; partly: some row sees a token that another does not)
+  // be where another row does (seen: bit ((i * NT + nt) * 2 + half) * RL + c; partly: some row sees a token that another
+  // does not)
   uint32_t seen = 0;
   bool partly = false;
   if (valid != (1u << CT) - 1u || pos < st.lo_all || pos + kTile * CT > st.hi_all) {
@@ -394,10 +418,11 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const bool see = (valid >> i & 1) && at >= st.lo[nt][c] && at < st.hi[nt][c];
-            if (see) seen |= 1u << ((i * NT + nt) * 4 + half * 2 + c);
-            else x[i][nt][half * 2 + c] = -CUDART_INF_F;
+          for (int c = 0; c < RL; ++c) {
+            const int p = st.pos[nt][c];
+            const bool see = (valid >> i & 1) && at >= begin_of(a, p) && at < end_of(a, p);
+            if (see) seen |= 1u << (((i * NT + nt) * 2 + half) * RL + c);
+            else x[i][nt][half][c] = -CUDART_INF_F;
             any |= see;
             all &= see;
           }
@@ -423,15 +448,15 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
 #pragma unroll
       for (int gi = 0; gi < NG; ++gi) top = __hmax2(top, *reinterpret_cast<const __half2 *>(&sv[i][half][gi]));
   const uint32_t top_bits = __half_as_ushort(__low2half(top));
-  float mx[NT][2];
+  float mx[NT][RL];
   bool more = static_cast<int>(top_bits >> 10) - 14 > st.e;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float v = fmaxf(x[0][nt][c], x[0][nt][2 + c]);
+    for (int c = 0; c < RL; ++c) {
+      float v = fmaxf(x[0][nt][0][c], x[0][nt][1][c]);
 #pragma unroll
-      for (int i = 1; i < CT; ++i) v = fmaxf(v, fmaxf(x[i][nt][c], x[i][nt][2 + c]));
+      for (int i = 1; i < CT; ++i) v = fmaxf(v, fmaxf(x[i][nt][0][c], x[i][nt][1][c]));
       mx[nt][c] = v;
       more |= fmaf(v, st.rs[nt][c], static_cast<float>(st.e - 15)) > st.m[nt][c];
     }
@@ -440,25 +465,26 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
     const float shift = static_cast<float>(e - st.e);
     st.e = e;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float al[RL];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < RL; ++c) {
         float v = mx[nt][c];
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
         const float mn = fmaxf(st.m[nt][c] + shift, fmaf(v, st.rs[nt][c], static_cast<float>(e - 11)));
-        const float al = exp2_approx(st.m[nt][c] - mn);
+        al[c] = exp2_approx(st.m[nt][c] - mn);
         st.m[nt][c] = mn;
-        st.l[nt][c] *= al;
+        st.l[nt][c] *= al[c];
 #pragma unroll
-        for (int gi = 0; gi < NG; ++gi) st.bias[nt][gi][c] *= al;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          st.acc[nt][k][c] *= al;
-          st.acc[nt][k][2 + c] *= al;
-        }
+        for (int gi = 0; gi < NG; ++gi) st.bias[nt][gi][c] *= al[c];
       }
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) st.acc[nt][k][c] *= al[F::kPair ? 0 : c & 1];
+    }
   }
   // --- weights, and their products with V
 #pragma unroll
@@ -466,33 +492,41 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        x[i][nt][c] = exp2_approx(fmaf(x[i][nt][c], st.rs[nt][c & 1], -st.m[nt][c & 1]));
-        st.l[nt][c & 1] += x[i][nt][c];
+      for (int c = 0; c < RL; ++c) {
+        x[i][nt][0][c] = exp2_approx(fmaf(x[i][nt][0][c], st.rs[nt][c], -st.m[nt][c]));
+        x[i][nt][1][c] = exp2_approx(fmaf(x[i][nt][1][c], st.rs[nt][c], -st.m[nt][c]));
+        st.l[nt][c] += x[i][nt][0][c] + x[i][nt][1][c];
       }
     const uint8_t *v = stage + i * F::kTileBytes + kTile * F::kRow + t * F::kRow + g * (F::kGroupBytes / 8);
+    uint32_t b[NT][2];
 #pragma unroll
     for (int gi = 0; gi < NG; ++gi) {
-      const float2 p0 = pair_of(sv[i][0][gi]), p1 = pair_of(sv[i][1][gi]);
-      uint32_t b[NT][2];
+      if (F::first_of(gi)) {
+        constexpr int GROUPS = F::kPair && NG > 1 ? 2 : 1;  // that share a fragment
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float y[4], z[4];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 sb = c < 2 ? p0 : p1;
-          y[c] = x[i][nt][c] * sb.x;
-          z[c] = x[i][nt][c] * sb.y;
-        }
-        if (partly) {
+          for (int half = 0; half < 2; ++half) {
+            float y[2] = {0.0f, 0.0f};  // (weight * scale) of the lane's two columns
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (!(seen >> ((i * NT + nt) * 4 + c) & 1)) y[c] = z[c] = 0.0f;
-        }
+            for (int gj = gi; gj < gi + GROUPS; ++gj) {
+              const float2 sb = pair_of(sv[i][half][gj]);
+              float z[RL];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) st.bias[nt][gi][c] += z[c] + z[2 + c];
-        b[nt][0] = transpose8x8(pack_half2(y[0], y[1]));
-        b[nt][1] = transpose8x8(pack_half2(y[2], y[3]));
+              for (int c = 0; c < RL; ++c) {
+                y[F::col(gj, c)] = x[i][nt][half][c] * sb.x;
+                z[c] = x[i][nt][half][c] * sb.y;
+              }
+              if (partly) {
+#pragma unroll
+                for (int c = 0; c < RL; ++c)
+                  if (!(seen >> (((i * NT + nt) * 2 + half) * RL + c) & 1)) y[F::col(gj, c)] = z[c] = 0.0f;
+              }
+#pragma unroll
+              for (int c = 0; c < RL; ++c) st.bias[nt][gj][c] += z[c];
+            }
+            b[nt][half] = transpose8x8(pack_half2(y[0], y[1]));
+          }
       }
       constexpr int VB = F::kGroupBytes / 8;        // bytes of a lane in a group of V: 2, 4, 8 or 16
       constexpr int VW = VB < 4 ? 1 : VB / 4;
@@ -531,15 +565,15 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, NT> &st, const uint8_t *stage, int po
   }
 }
 
-// Sums over the lanes that share rows, then the accumulator in its true size: acc[nt][k][c] becomes the weighted sum of
-// dimension (k / (G / 16)) * G + g * (G / 8) + 2 (k % (G / 16)) + c / 2 for row 8 nt + 2 t + c % 2.
-template <int BITS, int D, int G, int NT>
-AQ_DEVICE void finish_unit(State<BITS, D, G, NT> &st) {
-  using F = Form<BITS, D, G, NT>;
+// Sums over the lanes that share rows, then the accumulator in its true size: acc[nt][k][half * 2 + col(gi, c)] becomes the
+// weighted sum of dimension gi * G + g * (G / 8) + 2 (k % (G / 16)) + half, gi = k / (G / 16), for row row_of(nt, t, c).
+template <int BITS, int D, int G, int ROWS>
+AQ_DEVICE void finish_unit(State<BITS, D, G, ROWS> &st) {
+  using F = Form<BITS, D, G, ROWS>;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < F::kNT; ++nt)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < F::kRL; ++c) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         st.l[nt][c] += __shfl_xor_sync(0xffffffffu, st.l[nt][c], o);
@@ -548,16 +582,17 @@ AQ_DEVICE void finish_unit(State<BITS, D, G, NT> &st) {
       }
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const float b = st.bias[nt][k / (G / 16)][c];
-        st.acc[nt][k][c] = fmaf(st.acc[nt][k][c], 0x1p24f, b);
-        st.acc[nt][k][2 + c] = fmaf(st.acc[nt][k][2 + c], BITS == 4 ? 0x1p20f : 0x1p24f, b);
+        const int gi = k / (G / 16), col = F::col(gi, c);
+        const float b = st.bias[nt][gi][c];
+        st.acc[nt][k][col] = fmaf(st.acc[nt][k][col], 0x1p24f, b);
+        st.acc[nt][k][2 + col] = fmaf(st.acc[nt][k][2 + col], BITS == 4 ? 0x1p20f : 0x1p24f, b);
       }
     }
 }
 
 // Where row r of a unit goes: the flat row of out and lse.
 AQ_DEVICE int64_t out_row(const AttentionArgs &a, int seq, int h, int r) {
-  const int j = r / a.group, i = r - j * a.group;
+  const int j = a.tokens == 1 ? 0 : r / a.group, i = r - j * a.group;
   return (int64_t(seq) * a.tokens + j) * a.q_heads + h * a.group + i;
 }
 
@@ -565,15 +600,16 @@ AQ_DEVICE float log_sum(float m, float l) {
   return l > 0.0f ? (m + __log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
 }
 
-template <int BITS, int D, int G, int NT>
-AQ_DEVICE void write_out(const State<BITS, D, G, NT> &st, const AttentionArgs &a, int seq, int h, int row0) {
+template <int BITS, int D, int G, int ROWS>
+AQ_DEVICE void write_out(const State<BITS, D, G, ROWS> &st, const AttentionArgs &a, int seq, int h, int row0) {
+  using F = Form<BITS, D, G, ROWS>;
   constexpr int VE = G / 8;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < F::kNT; ++nt)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = row0 + nt * 8 + 2 * t + c;
+    for (int c = 0; c < F::kRL; ++c) {
+      const int r = row0 + F::row_of(nt, t, c);
       if (r >= a.tokens * a.group) continue;
       const int64_t row = out_row(a, seq, h, r);
       const float inv = st.l[nt][c] > 0.0f ? 1.0f / st.l[nt][c] : st.l[nt][c];  // (0 stays 0, NaN stays NaN)
@@ -582,8 +618,8 @@ AQ_DEVICE void write_out(const State<BITS, D, G, NT> &st, const AttentionArgs &a
         uint32_t u[VE / 2];
 #pragma unroll
         for (int k = 0; k < VE / 2; ++k) {
-          const float *acc = st.acc[nt][gi * (G / 16) + k];
-          const __nv_bfloat162 p = __floats2bfloat162_rn(acc[c] * inv, acc[2 + c] * inv);
+          const float *acc = st.acc[nt][gi * (G / 16) + k] + F::col(gi, c);
+          const __nv_bfloat162 p = __floats2bfloat162_rn(acc[0] * inv, acc[2] * inv);
           u[k] = *reinterpret_cast<const uint32_t *>(&p);
         }
         uint16_t *dst = a.out + row * D + gi * G + g * VE;
@@ -599,25 +635,26 @@ AQ_DEVICE void write_out(const State<BITS, D, G, NT> &st, const AttentionArgs &a
     }
 }
 
-// A partial result: kRows references, kRows sums, then [kRows][D].
-template <int BITS, int D, int G, int NT>
-AQ_DEVICE void write_part(const State<BITS, D, G, NT> &st, float *part) {
-  using F = Form<BITS, D, G, NT>;
+// A partial result: ROWS references, ROWS sums, then [ROWS][D].
+template <int BITS, int D, int G, int ROWS>
+AQ_DEVICE void write_part(const State<BITS, D, G, ROWS> &st, float *part) {
+  using F = Form<BITS, D, G, ROWS>;
   constexpr int VE = G / 8;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < F::kNT; ++nt)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = nt * 8 + 2 * t + c;
-      if (g == 0) part[r] = st.m[nt][c], part[F::kRows + r] = st.l[nt][c];
+    for (int c = 0; c < F::kRL; ++c) {
+      const int r = F::row_of(nt, t, c);
+      if (g == 0) part[r] = st.m[nt][c], part[ROWS + r] = st.l[nt][c];
 #pragma unroll
       for (int gi = 0; gi < D / G; ++gi) {
-        float4 *dst = reinterpret_cast<float4 *>(part + 2 * F::kRows + r * D + gi * G + g * VE);
+        float4 *dst = reinterpret_cast<float4 *>(part + 2 * ROWS + r * D + gi * G + g * VE);
 #pragma unroll
         for (int k = 0; k < VE / 4; ++k) {
-          const float *x = st.acc[nt][gi * (G / 16) + 2 * k], *y = st.acc[nt][gi * (G / 16) + 2 * k + 1];
-          dst[k] = make_float4(x[c], x[2 + c], y[c], y[2 + c]);
+          const int col = F::col(gi, c);
+          const float *x = st.acc[nt][gi * (G / 16) + 2 * k] + col, *y = st.acc[nt][gi * (G / 16) + 2 * k + 1] + col;
+          dst[k] = make_float4(x[0], x[2], y[0], y[2]);
         }
       }
     }
@@ -679,10 +716,10 @@ struct Cursor {
   }
 };
 
-template <int BITS, int D, int G, int NT>
-__global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
+template <int BITS, int D, int G, int ROWS>
+__global__ void __launch_bounds__(kThreads, Form<BITS, D, G, ROWS>::kCtas)
     attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Plan plan) {
-  using F = Form<BITS, D, G, NT>;
+  using F = Form<BITS, D, G, ROWS>;
   constexpr int CT = F::kCT, CHUNK = CT * kTile;
   extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings
   __shared__ uint64_t bars[kWarps][F::kStages];
@@ -797,28 +834,28 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
         if (left <= 0) return;
         ahead.next_unit(a, plan.row_tiles);
         pos_in = ahead.span.first * CHUNK + lane * kTile;
-        prefetch_queries<D, NT>(a, ahead.seq, ahead.head, ahead.row_tile * F::kRows);
+        prefetch_queries<D, ROWS>(a, ahead.seq, ahead.head, ahead.row_tile * ROWS);
       }
       if (left > 0) look_up();
     };
     look_up();
-    Queries<BITS, D, G, NT> queries;
-    load_queries(queries, a, cur.seq, cur.head, cur.row_tile * F::kRows);
+    Queries<BITS, D, G, ROWS> queries;
+    load_queries(queries, a, cur.seq, cur.head, cur.row_tile * ROWS);
     for (int i = 0; i < F::kStages && left > 0; ++i) issue();
     // --- the run, unit by unit
     bool ok = true;
     int at = begin, stage = 0, parity = 0;
     while (true) {
-      const int row0 = cur.row_tile * F::kRows;
+      const int row0 = cur.row_tile * ROWS;
       const int first = cur.chunk, take = min(cur.span.chunks - first, end - at);
-      State<BITS, D, G, NT> st;
+      State<BITS, D, G, ROWS> st;
       start_unit(st, queries, a, cur.span.len, row0);
       int pos = (cur.span.first + first) * CHUNK;
       for (int i = 0; i < take; ++i, pos += CHUNK) {
         ok = mbar_wait(&bars[warp][stage], parity, &abort_flag, &g_fault, kFaultQmvWait);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        run_chunk(st, ring + stage * F::kStage, pos, valid_bits & ((1u << CT) - 1u));
+        run_chunk(st, a, ring + stage * F::kStage, pos, valid_bits & ((1u << CT) - 1u));
         __syncwarp();
         --flying;
         valid_bits >>= CT;
@@ -848,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
       at += kUnitCost;  // the next unit's first chunk
       if (at >= end) break;
       cur.next_unit(a, plan.row_tiles);
-      load_queries(queries, a, cur.seq, cur.head, cur.row_tile * F::kRows);
+      load_queries(queries, a, cur.seq, cur.head, cur.row_tile * ROWS);
     }
     if (!ok) {  // copies in flight land before the CTA goes
       for (; flying > 0; --flying) {
@@ -878,14 +915,14 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
       auto part = [&](int k) -> const float * {
         return ends && k == n - 1 ? end_part : reinterpret_cast<const float *>(smem + ((first >> 1) + k) * F::kRing);
       };
-      const int seq = id / units, u = id - seq * units, h = u / plan.row_tiles, row0 = (u - h * plan.row_tiles) * F::kRows;
+      const int seq = id / units, u = id - seq * units, h = u / plan.row_tiles, row0 = (u - h * plan.row_tiles) * ROWS;
       float *dst = plan.parts + (int64_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * F::kPart;
-      join<F::kRows, D>(n, part, [&](int r, int c, float4 o, float m, float l) {
+      join<ROWS, D>(n, part, [&](int r, int c, float4 o, float m, float l) {
         if (starts && ends) {
           put_out<D>(a, seq, h, row0 + r, c, o, m, l);
         } else {
-          if (c == 0) dst[r] = m, dst[F::kRows + r] = l;
-          reinterpret_cast<float4 *>(dst + 2 * F::kRows)[r * (D / 4) + c] = o;
+          if (c == 0) dst[r] = m, dst[ROWS + r] = l;
+          reinterpret_cast<float4 *>(dst + 2 * ROWS)[r * (D / 4) + c] = o;
         }
       });
       if (starts && !ends) loose = Loose{id, (tail_end[first >> 1] - 1) / (kWarps * share)};
@@ -896,10 +933,10 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, NT>::kCtas)
 
 // Joins the units that several CTAs have a part of: block (i, r) takes row r of the one that starts in CTA i's run and
 // goes on behind it.  Threads share the parts (there are up to as many as CTAs) as well as the columns.
-template <int D, int NT>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ AttentionArgs a,
                                                         const __grid_constant__ Plan plan) {
-  constexpr int ROWS = 8 * NT, PART = ROWS * (D + 2), COLS = D / 4, SHARES = kThreads / COLS, MOST = 2 * kSms;
+  constexpr int PART = ROWS * (D + 2), COLS = D / 4, SHARES = kThreads / COLS, MOST = 2 * kSms;
   __shared__ float weights[MOST], red[2][kWarps];
   __shared__ float4 sums[SHARES][COLS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = blockIdx.y, cta = blockIdx.x;
@@ -968,11 +1005,11 @@ struct Sizes {
   size_t parts, heads, loose, bytes;  // offsets of the workspace's parts, and its size
 };
 
-template <int BITS, int D, int G, int NT>
+template <int BITS, int D, int G, int ROWS>
 Sizes sizes_of(const AttentionArgs &a) {
-  using F = Form<BITS, D, G, NT>;
+  using F = Form<BITS, D, G, ROWS>;
   Sizes s;
-  s.row_tiles = (a.tokens * a.group + F::kRows - 1) / F::kRows;
+  s.row_tiles = (a.tokens * a.group + ROWS - 1) / ROWS;
   const int64_t units = int64_t(a.c.batch) * a.c.heads * s.row_tiles, slots = int64_t(kSms) * F::kCtas;
   // chunks that a unit can have
   int64_t most = ((int64_t(a.c.width) << a.c.page_shift) + F::kCT * kTile - 1) / (F::kCT * kTile);
@@ -987,10 +1024,10 @@ Sizes sizes_of(const AttentionArgs &a) {
   return s;
 }
 
-template <int BITS, int D, int G, int NT>
+template <int BITS, int D, int G, int ROWS>
 cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
-  using F = Form<BITS, D, G, NT>;
-  auto kern = attention_kernel<BITS, D, G, NT>;
+  using F = Form<BITS, D, G, ROWS>;
+  auto kern = attention_kernel<BITS, D, G, ROWS>;
   constexpr int kBytes = kWarps * F::kRing;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1002,7 +1039,7 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  const Sizes s = sizes_of<BITS, D, G, NT>(a);
+  const Sizes s = sizes_of<BITS, D, G, ROWS>(a);
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   Plan plan;
   plan.ctas = s.ctas;
@@ -1015,7 +1052,7 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
   if ((e = cudaGetLastError()) != cudaSuccess || s.direct || s.ctas == 1) return e;
   // The join starts while the last CTAs run, and waits for them.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(s.ctas, 8 * NT);
+  cfg.gridDim = dim3(s.ctas, ROWS);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1023,39 +1060,40 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, a, plan);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, ROWS>, a, plan);
 }
 
-// Calls run for a form: two column tiles of query rows where a KV head has more than eight rows and
-// the accumulators of both fit a thread's registers.
+// Calls run for a form: as many rows as a KV head has, up to 16 (8 where the accumulators of 16 rows do not fit a thread's
+// registers).
+template <int D, int G, class Run>
+auto by_rows(const AttentionArgs &a, Run run) {
+  const int64_t rows = a.tokens * int64_t(a.group);
+  if (rows <= 4) return run(Int<D>{}, Int<G>{}, Int<4>{});
+  if (rows <= 8 || D > 128) return run(Int<D>{}, Int<G>{}, Int<8>{});
+  return run(Int<D>{}, Int<G>{}, Int<(D > 128 ? 8 : 16)>{});
+}
 template <class Run>
 auto by_form(const AttentionArgs &a, int D, int G, Run run) {
-  const bool two = a.tokens * int64_t(a.group) > 8;
-  if (D == 64) {
-    if (G == 32) return two ? run(Int<64>{}, Int<32>{}, Int<2>{}) : run(Int<64>{}, Int<32>{}, Int<1>{});
-    return two ? run(Int<64>{}, Int<64>{}, Int<2>{}) : run(Int<64>{}, Int<64>{}, Int<1>{});
-  }
+  if (D == 64) return G == 32 ? by_rows<64, 32>(a, run) : by_rows<64, 64>(a, run);
   if (D == 128) {
-    if (G == 32) return two ? run(Int<128>{}, Int<32>{}, Int<2>{}) : run(Int<128>{}, Int<32>{}, Int<1>{});
-    if (G == 64) return two ? run(Int<128>{}, Int<64>{}, Int<2>{}) : run(Int<128>{}, Int<64>{}, Int<1>{});
-    return two ? run(Int<128>{}, Int<128>{}, Int<2>{}) : run(Int<128>{}, Int<128>{}, Int<1>{});
+    if (G == 32) return by_rows<128, 32>(a, run);
+    return G == 64 ? by_rows<128, 64>(a, run) : by_rows<128, 128>(a, run);
   }
-  if (G == 32) return run(Int<256>{}, Int<32>{}, Int<1>{});
-  if (G == 64) return run(Int<256>{}, Int<64>{}, Int<1>{});
-  return run(Int<256>{}, Int<128>{}, Int<1>{});
+  if (G == 32) return by_rows<256, 32>(a, run);
+  return G == 64 ? by_rows<256, 64>(a, run) : by_rows<256, 128>(a, run);
 }
 
 template <int BITS>
 cudaError_t launch_bits(const AttentionArgs &a, int D, int G, cudaStream_t s) {
-  return by_form(a, D, G, [&](auto d, auto g, auto nt) {
-    return launch_form<BITS, decltype(d)::value, decltype(g)::value, decltype(nt)::value>(a, s);
+  return by_form(a, D, G, [&](auto d, auto g, auto r) {
+    return launch_form<BITS, decltype(d)::value, decltype(g)::value, decltype(r)::value>(a, s);
   });
 }
 
 template <int BITS>
 size_t workspace_bits(const AttentionArgs &a, int D, int G) {
-  return by_form(a, D, G, [&](auto d, auto g, auto nt) {
-    return sizes_of<BITS, decltype(d)::value, decltype(g)::value, decltype(nt)::value>(a).bytes;
+  return by_form(a, D, G, [&](auto d, auto g, auto r) {
+    return sizes_of<BITS, decltype(d)::value, decltype(g)::value, decltype(r)::value>(a).bytes;
   });
 }
 
