@@ -660,27 +660,33 @@ AQ_DEVICE void write_part(const State<BITS, D, G, ROWS> &st, float *part) {
     }
 }
 
-// Joins n partial results, part(0) .. part(n - 1) in this order: calls put(row, column / 4, sum, reference, weights'
-// sum) for every four columns.  All threads of the CTA.  (Run once, so its loops stay loops: instructions that are new to
-// an SM cost more than their steps.)
+// Joins row r of n <= 32 partial results, part(0) .. part(n - 1) in this order, by one warp: calls put(column / 4, sum,
+// reference, weights' sum) for every four columns.
 template <int ROWS, int D, class Part, class Put>
-AQ_DEVICE void join(int n, Part part, Put put) {
+AQ_DEVICE void join_row(int n, int r, Part part, Put put) {
+  const int lane = threadIdx.x & 31;
+  const float *mine = part(min(lane, n - 1));
+  const float mk = lane < n ? mine[r] : -1e30f, lk = lane < n ? mine[ROWS + r] : 0.0f;
+  float m = mk;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float wk = exp2_approx(mk - m);
+  float l = wk * lk;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll 1
-  for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
-    const int r = i / (D / 4), c = i - r * (D / 4);
-    float m = -1e30f, l = 0.0f;
-#pragma unroll 2
-    for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[r]);
+  for (int c0 = 0; c0 < D / 4; c0 += 32) {
+    const int c = c0 + lane;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const float *p = part(k);
-      const float w = exp2_approx(p[r] - m);
-      const float4 v = reinterpret_cast<const float4 *>(p + 2 * ROWS)[i];
-      l = fmaf(w, p[ROWS + r], l);
-      o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+      const float w = __shfl_sync(0xffffffffu, wk, k);
+      if (c < D / 4) {
+        const float4 v = reinterpret_cast<const float4 *>(part(k) + 2 * ROWS + r * D)[c];
+        o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+      }
     }
-    put(r, c, o, m, l);
+    if (c < D / 4) put(c, o, m, l);
   }
 }
 
@@ -900,32 +906,36 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, ROWS>::kCtas)
   Loose loose{-1, -1};
   if (!abort_flag) {
     // slot 2 w: warp w's head, slot 2 w + 1: its tail; lane s looks at slot s
-    const int slot = lane & 15, mine = slot & 1 ? tail_unit[slot >> 1] : head_unit[slot >> 1];
-    const uint32_t used = __ballot_sync(0xffffffffu, mine >= 0) & 0xFFFFu, below = used & ((1u << slot) - 1u);
+    static_assert(2 * kWarps <= 32, "a lane for each slot");
+    const int mine = lane >= 2 * kWarps ? -1 : lane & 1 ? tail_unit[lane >> 1] : head_unit[lane >> 1];
+    const uint32_t used = __ballot_sync(0xffffffffu, mine >= 0), below = used & ((1u << lane) - 1u);
     const int before = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
-    uint32_t firsts = __ballot_sync(0xffffffffu, mine >= 0 && (!below || before != mine)) & 0xFFFFu;
-    while (firsts) {
+    uint32_t firsts = __ballot_sync(0xffffffffu, mine >= 0 && (!below || before != mine));
+    for (int base = 0; firsts; base += ROWS) {
       // a unit's parts lie in warps that follow one another, one in each; only the last of them can be a head
       const int first = __ffs(firsts) - 1;
       firsts &= firsts - 1;
-      const uint32_t members = used & ((firsts ? firsts & -firsts : 0x10000u) - (1u << first));
+      const uint32_t members = used & ((firsts & -firsts) - 1u) & ~((1u << first) - 1u);  // (0 - 1: all the rest)
       const int n = __popc(members), last = 31 - __clz(members), id = __shfl_sync(0xffffffffu, mine, first);
       const bool starts = (first & 1) && tail_starts[first >> 1], ends = !(last & 1);
+      if (starts && !ends) loose = Loose{id, (tail_end[first >> 1] - 1) / (kWarps * share)};
       const float *end_part = plan.heads + (int64_t(blockIdx.x) * kWarps + (last >> 1)) * F::kPart;
       auto part = [&](int k) -> const float * {
         return ends && k == n - 1 ? end_part : reinterpret_cast<const float *>(smem + ((first >> 1) + k) * F::kRing);
       };
       const int seq = id / units, u = id - seq * units, h = u / plan.row_tiles, row0 = (u - h * plan.row_tiles) * ROWS;
       float *dst = plan.parts + (int64_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * F::kPart;
-      join<ROWS, D>(n, part, [&](int r, int c, float4 o, float m, float l) {
-        if (starts && ends) {
-          put_out<D>(a, seq, h, row0 + r, c, o, m, l);
-        } else {
-          if (c == 0) dst[r] = m, dst[ROWS + r] = l;
-          reinterpret_cast<float4 *>(dst + 2 * ROWS)[r * (D / 4) + c] = o;
-        }
-      });
-      if (starts && !ends) loose = Loose{id, (tail_end[first >> 1] - 1) / (kWarps * share)};
+      // the units' rows, one after the other, go around the warps
+      for (int r = (warp + kWarps - base % kWarps) % kWarps; r < ROWS; r += kWarps) {
+        join_row<ROWS, D>(n, r, part, [&](int c, float4 o, float m, float l) {
+          if (starts && ends) {
+            put_out<D>(a, seq, h, row0 + r, c, o, m, l);
+          } else {
+            if (c == 0) dst[r] = m, dst[ROWS + r] = l;
+            reinterpret_cast<float4 *>(dst + 2 * ROWS)[r * (D / 4) + c] = o;
+          }
+        });
+      }
     }
   }
   if (threadIdx.x == 0 && !plan.direct) plan.loose[blockIdx.x] = loose;
