@@ -47,8 +47,11 @@ __device__ uint32_t g_fault = 0;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSms = 148;  // the grid never has more CTAs than these hold
-// Units of at most so many chunks, and no more of them than CTAs, get a CTA each: no list of places, no second kernel.
-constexpr int kDirectChunks = 2 * kWarps;
+// Units that cannot have more tokens than this, and are no more than the GPU holds CTAs, get a CTA each: no list of places, no
+// second kernel.  Measured at 4 bits, D = 128, four query rows, against the list: 8 to 256 units of 128 tokens 5.2 to 6.4 us
+// against 9.3 to 11.4 us, of 1024 tokens 9.8 to 14.9 against 9.2 to 19.0 us; of 2048 tokens 14.7 against 9.2 us at 8 units, 14.9
+// against 13.5 us at 64, 15.9 against 18.2 us at 128 and 22.7 against 28.1 us at 256.
+constexpr int kDirectTokens = 1024, kDirectTokensOfMany = 2048, kMany = 128;
 
 // ROWS: query rows that a unit takes, 4, 8 or 16.
 template <int BITS, int D, int G, int ROWS>
@@ -660,33 +663,50 @@ AQ_DEVICE void write_part(const State<BITS, D, G, ROWS> &st, float *part) {
     }
 }
 
-// Joins row r of n <= 32 partial results, part(0) .. part(n - 1) in this order, by one warp: calls put(column / 4, sum,
-// reference, weights' sum) for every four columns.
-template <int ROWS, int D, class Part, class Put>
-AQ_DEVICE void join_row(int n, int r, Part part, Put put) {
-  const int lane = threadIdx.x & 31;
-  const float *mine = part(min(lane, n - 1));
-  const float mk = lane < n ? mine[r] : -1e30f, lk = lane < n ? mine[ROWS + r] : 0.0f;
-  float m = mk;
+// Joins rows r0, r0 + STEP, .. (RN of them) of n <= kWarps partial results, part(0) .. part(n - 1) in this order, by one
+// warp: calls put(row, column / 4, sum, reference, weights' sum) for every four columns.  The rows are gone through together,
+// for their loads and shuffles wait for one another.
+template <int ROWS, int D, int RN, int STEP, class Part, class Put>
+AQ_DEVICE void join_rows(int n, int r0, Part part, Put put) {
+  static_assert((kWarps & (kWarps - 1)) == 0 && kWarps <= 32, "lanes repeat the parts");
+  const int lane = threadIdx.x & 31, mine = lane % kWarps;  // this lane's part
+  float m[RN], l[RN], wk[RN];
+  const float *p = part(min(mine, n - 1));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float wk = exp2_approx(mk - m);
-  float l = wk * lk;
+  for (int i = 0; i < RN; ++i) {
+    m[i] = wk[i] = mine < n ? p[r0 + i * STEP] : -1e30f;
+    l[i] = mine < n ? p[ROWS + r0 + i * STEP] : 0.0f;
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-#pragma unroll 1
+  for (int o = kWarps / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < RN; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+  for (int i = 0; i < RN; ++i) wk[i] = exp2_approx(wk[i] - m[i]), l[i] *= wk[i];
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < RN; ++i) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+#pragma unroll
   for (int c0 = 0; c0 < D / 4; c0 += 32) {
     const int c = c0 + lane;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const bool active = D / 4 % 32 == 0 || c < D / 4;
+    float4 o[RN] = {};
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const float w = __shfl_sync(0xffffffffu, wk, k);
-      if (c < D / 4) {
-        const float4 v = reinterpret_cast<const float4 *>(part(k) + 2 * ROWS + r * D)[c];
-        o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+      const float4 *v = reinterpret_cast<const float4 *>(part(k) + 2 * ROWS) + c;
+#pragma unroll
+      for (int i = 0; i < RN; ++i) {
+        const float w = __shfl_sync(0xffffffffu, wk[i], k);
+        const float4 x = active ? v[(r0 + i * STEP) * (D / 4)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        o[i].x = fmaf(w, x.x, o[i].x), o[i].y = fmaf(w, x.y, o[i].y);
+        o[i].z = fmaf(w, x.z, o[i].z), o[i].w = fmaf(w, x.w, o[i].w);
       }
     }
-    if (c < D / 4) put(c, o, m, l);
+    if (active) {
+#pragma unroll
+      for (int i = 0; i < RN; ++i) put(r0 + i * STEP, c, o[i], m[i], l[i]);
+    }
   }
 }
 
@@ -926,8 +946,10 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, ROWS>::kCtas)
       const int seq = id / units, u = id - seq * units, h = u / plan.row_tiles, row0 = (u - h * plan.row_tiles) * ROWS;
       float *dst = plan.parts + (int64_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * F::kPart;
       // the units' rows, one after the other, go around the warps
-      for (int r = (warp + kWarps - base % kWarps) % kWarps; r < ROWS; r += kWarps) {
-        join_row<ROWS, D>(n, r, part, [&](int c, float4 o, float m, float l) {
+      constexpr int RN = ROWS > kWarps ? ROWS / kWarps : 1;
+      const int r0 = (warp + kWarps - base % kWarps) % kWarps;
+      if (r0 < ROWS) {
+        join_rows<ROWS, D, RN, kWarps>(n, r0, part, [&](int r, int c, float4 o, float m, float l) {
           if (starts && ends) {
             put_out<D>(a, seq, h, row0 + r, c, o, m, l);
           } else {
@@ -1024,7 +1046,7 @@ Sizes sizes_of(const AttentionArgs &a) {
   // chunks that a unit can have
   int64_t most = ((int64_t(a.c.width) << a.c.page_shift) + F::kCT * kTile - 1) / (F::kCT * kTile);
   if (a.window) most = std::min<int64_t>(most, (int64_t(a.window) + a.tokens) / (F::kCT * kTile) + 2);
-  s.direct = units <= slots && most <= kDirectChunks;
+  s.direct = units <= slots && most * F::kCT * kTile <= (units >= kMany ? kDirectTokensOfMany : kDirectTokens);
   // a CTA has a place for each of its warps at least
   s.ctas = static_cast<int>(s.direct ? units : std::min<int64_t>((units * (most + kUnitCost) + kWarps - 1) / kWarps, slots));
   s.parts = 0;
