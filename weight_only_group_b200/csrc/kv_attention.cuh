@@ -44,14 +44,18 @@ namespace {
 
 __device__ uint32_t g_fault = 0;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kSms = 148;  // the grid never has more CTAs than these hold
-// Units that cannot have more tokens than this, and are no more than the GPU holds CTAs, get a CTA each: no list of places, no
-// second kernel.  Measured at 4 bits, D = 128, four query rows, against the list: 8 to 256 units of 128 tokens 5.2 to 6.4 us
-// against 9.3 to 11.4 us, of 1024 tokens 9.8 to 14.9 against 9.2 to 19.0 us; of 2048 tokens 14.7 against 9.2 us at 8 units, 14.9
-// against 13.5 us at 64, 15.9 against 18.2 us at 128 and 22.7 against 28.1 us at 256.
-constexpr int kDirectTokens = 1024, kDirectTokensOfMany = 2048, kMany = 128;
+constexpr int kSms = 148;         // the grid never has more CTAs than these hold
+constexpr int kMostCtas = 3;      // of an SM
+constexpr int kJoinThreads = 256;
+// Where units are no more than the GPU holds CTAs, and none can have more than this many bytes of cache for each warp of a
+// CTA (twice as many where there are enough units for nearly every SM), a CTA takes a unit: no list of places, no second
+// kernel.  Measured against the list (4 bits, D = 128, four rows, 8 warps: 4 chunks of 32 tokens a warp are 1024 tokens): 8
+// to 256 units of 128 tokens 5.2 to 6.4 us against 9.3 to 11.4 us, of 1024 tokens 9.8 to 14.9 against 9.2 to 19.0 us; of 2048
+// tokens 14.7 against 9.2 us at 8 units, 14.9 against 13.5 us at 64, 15.9 against 18.2 us at 128.  Eight rows, 4 warps: 8
+// units of 512 tokens 8.8 against 9.1 us, of 1024 13.2 against 9.6 us; D = 256: of 512 tokens 11.0 against 12.0 us, of 1024
+// 15.4 against 12.1 us.
+constexpr int64_t kDirectBytes = 4 * 4608;
+constexpr int kMany = 128;
 
 // ROWS: query rows that a unit takes, 4, 8 or 16.
 template <int BITS, int D, int G, int ROWS>
@@ -75,12 +79,20 @@ struct Form {
   static constexpr int kCT = kTileBytes > 4800 ? 1 : 2;
   static constexpr int kStage = kCT * kTileBytes;
   static constexpr int kPart = ROWS * (D + 2);       // floats of a partial result: max, sum, accumulator
-  // Two CTAs on an SM where their rings have two stages or more and 128 registers a thread hold the accumulator.
+  // Warps of a CTA and CTAs of an SM: 16 warps of 128 registers for four rows, 12 of 168 for eight, whose accumulators and
+  // queries take 24 more, and 8 of 255 where an accumulator, or a ring of three stages, leaves no room for more.  Measured:
+  // 64 ragged sequences, 4 bits, four rows 68.3 us at 16 warps and 71.7 at 12; eight rows 87.7 and 86.4 (up to 1500 tokens
+  // 32.5 and 27.9); 8 bits and D = 128, 32 sequences, eight rows 120 us at 8 warps, 122 at 12 and 128 at 16 (these two with
+  // chunks of one tile).
   static constexpr int kSmem = 224 * 1024;
-  static constexpr int kCtas = (ROWS <= 8 && D <= 128 && kSmem / 2 / (kWarps * kStage) >= 2) ? 2 : 1;
+  static constexpr bool kSmall = D <= 128 && kSmem / (12 * kStage) >= 3;
+  static constexpr int kWarps = kSmall && ROWS == 8 ? 4 : 8;
+  static constexpr int kCtas = !kSmall || ROWS == 16 ? 1 : ROWS == 8 ? 3 : 2;
+  static constexpr int kThreads = kWarps * 32;
   static constexpr int kStages = kSmem / kCtas / (kWarps * kStage) > 4 ? 4 : kSmem / kCtas / (kWarps * kStage);
   static constexpr int kRing = kStages * kStage;     // bytes of a warp's ring
   static_assert(kStages >= 2 && kRing >= kPart * 4, "a warp's ring holds two stages, and its last partial result");
+  static_assert(kCtas <= kMostCtas, "the join kernel's room for parts");
 };
 
 // What a CTA leaves for the join: the unit that starts in its run and goes on
@@ -666,7 +678,7 @@ AQ_DEVICE void write_part(const State<BITS, D, G, ROWS> &st, float *part) {
 // Joins rows r0, r0 + STEP, .. (RN of them) of n <= kWarps partial results, part(0) .. part(n - 1) in this order, by one
 // warp: calls put(row, column / 4, sum, reference, weights' sum) for every four columns.  The rows are gone through together,
 // for their loads and shuffles wait for one another.
-template <int ROWS, int D, int RN, int STEP, class Part, class Put>
+template <int kWarps, int ROWS, int D, int RN, int STEP, class Part, class Put>
 AQ_DEVICE void join_rows(int n, int r0, Part part, Put put) {
   static_assert((kWarps & (kWarps - 1)) == 0 && kWarps <= 32, "lanes repeat the parts");
   const int lane = threadIdx.x & 31, mine = lane % kWarps;  // this lane's part
@@ -743,10 +755,10 @@ struct Cursor {
 };
 
 template <int BITS, int D, int G, int ROWS>
-__global__ void __launch_bounds__(kThreads, Form<BITS, D, G, ROWS>::kCtas)
+__global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D, G, ROWS>::kCtas)
     attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Plan plan) {
   using F = Form<BITS, D, G, ROWS>;
-  constexpr int CT = F::kCT, CHUNK = CT * kTile;
+  constexpr int CT = F::kCT, CHUNK = CT * kTile, kWarps = F::kWarps, kThreads = F::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings
   __shared__ uint64_t bars[kWarps][F::kStages];
   __shared__ int sums[kThreads + 1], warp_sums[kWarps];
@@ -949,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, ROWS>::kCtas)
       constexpr int RN = ROWS > kWarps ? ROWS / kWarps : 1;
       const int r0 = (warp + kWarps - base % kWarps) % kWarps;
       if (r0 < ROWS) {
-        join_rows<ROWS, D, RN, kWarps>(n, r0, part, [&](int r, int c, float4 o, float m, float l) {
+        join_rows<kWarps, ROWS, D, RN, kWarps>(n, r0, part, [&](int r, int c, float4 o, float m, float l) {
           if (starts && ends) {
             put_out<D>(a, seq, h, row0 + r, c, o, m, l);
           } else {
@@ -966,9 +978,10 @@ __global__ void __launch_bounds__(kThreads, Form<BITS, D, G, ROWS>::kCtas)
 // Joins the units that several CTAs have a part of: block (i, r) takes row r of the one that starts in CTA i's run and
 // goes on behind it.  Threads share the parts (there are up to as many as CTAs) as well as the columns.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ AttentionArgs a,
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttentionArgs a,
                                                         const __grid_constant__ Plan plan) {
-  constexpr int PART = ROWS * (D + 2), COLS = D / 4, SHARES = kThreads / COLS, MOST = 2 * kSms;
+  constexpr int PART = ROWS * (D + 2), COLS = D / 4, kThreads = kJoinThreads, kWarps = kThreads / 32;
+  constexpr int SHARES = kThreads / COLS, MOST = kMostCtas * kSms;
   __shared__ float weights[MOST], red[2][kWarps];
   __shared__ float4 sums[SHARES][COLS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = blockIdx.y, cta = blockIdx.x;
@@ -1040,13 +1053,14 @@ struct Sizes {
 template <int BITS, int D, int G, int ROWS>
 Sizes sizes_of(const AttentionArgs &a) {
   using F = Form<BITS, D, G, ROWS>;
+  constexpr int kWarps = F::kWarps;
   Sizes s;
   s.row_tiles = (a.tokens * a.group + ROWS - 1) / ROWS;
   const int64_t units = int64_t(a.c.batch) * a.c.heads * s.row_tiles, slots = int64_t(kSms) * F::kCtas;
   // chunks that a unit can have
   int64_t most = ((int64_t(a.c.width) << a.c.page_shift) + F::kCT * kTile - 1) / (F::kCT * kTile);
   if (a.window) most = std::min<int64_t>(most, (int64_t(a.window) + a.tokens) / (F::kCT * kTile) + 2);
-  s.direct = units <= slots && most * F::kCT * kTile <= (units >= kMany ? kDirectTokensOfMany : kDirectTokens);
+  s.direct = units <= slots && most * F::kStage <= kDirectBytes * kWarps * (units >= kMany ? 2 : 1);
   // a CTA has a place for each of its warps at least
   s.ctas = static_cast<int>(s.direct ? units : std::min<int64_t>((units * (most + kUnitCost) + kWarps - 1) / kWarps, slots));
   s.parts = 0;
@@ -1060,7 +1074,7 @@ template <int BITS, int D, int G, int ROWS>
 cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
   using F = Form<BITS, D, G, ROWS>;
   auto kern = attention_kernel<BITS, D, G, ROWS>;
-  constexpr int kBytes = kWarps * F::kRing;
+  constexpr int kBytes = F::kWarps * F::kRing;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1080,12 +1094,12 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
   plan.parts = reinterpret_cast<float *>(ws + s.parts);
   plan.heads = reinterpret_cast<float *>(ws + s.heads);
   plan.loose = reinterpret_cast<Loose *>(ws + s.loose);
-  kern<<<s.ctas, kThreads, kBytes, stream>>>(a, plan);
+  kern<<<s.ctas, F::kThreads, kBytes, stream>>>(a, plan);
   if ((e = cudaGetLastError()) != cudaSuccess || s.direct || s.ctas == 1) return e;
   // The join starts while the last CTAs run, and waits for them.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(s.ctas, ROWS);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1095,13 +1109,14 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, join_kernel<D, ROWS>, a, plan);
 }
 
-// Calls run for a form: as many rows as a KV head has, up to 16 (8 where the accumulators of 16 rows do not fit a thread's
-// registers).
+// Calls run for a form: as many rows as a KV head has, up to 16; 8 where the accumulators of 16 rows do not fit a thread's
+// registers, and for 17 to 24 rows, three times 8 (five tokens, 20 rows, 4 bits: 16 sequences up to 3001 tokens 41.9 us, and
+// 45.5 us in two times 16).
 template <int D, int G, class Run>
 auto by_rows(const AttentionArgs &a, Run run) {
   const int64_t rows = a.tokens * int64_t(a.group);
   if (rows <= 4) return run(Int<D>{}, Int<G>{}, Int<4>{});
-  if (rows <= 8 || D > 128) return run(Int<D>{}, Int<G>{}, Int<8>{});
+  if (rows <= 8 || D > 128 || (rows > 16 && rows <= 24)) return run(Int<D>{}, Int<G>{}, Int<8>{});
   return run(Int<D>{}, Int<G>{}, Int<(D > 128 ? 8 : 16)>{});
 }
 template <class Run>
