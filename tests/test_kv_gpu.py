@@ -444,6 +444,56 @@ def test_captured_and_replayed():
     assert np.array_equal(data.cpu().numpy(), c.data)
 
 
+@pytest.mark.parametrize("captured", (False, True))
+def test_steps_that_follow_one_another(captured):
+    """Steps queued without a wait between them: each kernel reads what the one just before it wrote (lengths, tokens,
+    queries, the cache).  The same bits as with a wait after every call."""
+    D, G, bits, H, Hq, B, steps = 64, 32, 4, 4, 8, 3, 24
+    c = filled([40, 300, 7], heads=H, page_size=16, D=D, G=G, bits=bits, seed=61, width=24)
+    tokens = torch.randn(steps, 3, B, Hq, D, device="cuda").bfloat16()
+
+    def run(wait):
+        data, table, ln = on_gpu(c)
+        q, k, v = (torch.empty(B, x, D, dtype=torch.bfloat16, device="cuda") for x in (Hq, H, H))
+        last = torch.zeros(B, Hq, D, dtype=torch.bfloat16, device="cuda")
+        outs = []
+
+        def step(i):
+            ln.add_(1)
+            torch.add(tokens[i, 0], last, out=q)  # the step before goes into this one
+            k.copy_(tokens[i, 1][:, :H])
+            v.copy_(tokens[i, 2][:, :H])
+            wait()
+            aq.aq_kv_append(data, k, v, table, ln, G, bits)
+            wait()
+            aq.aq_kv_attention(q, data, table, ln, G, bits, out=last)
+            wait()
+            kr, vr = aq.aq_kv_read(data, table, ln, B, D, G, bits)
+            wait()
+            outs.append((last.clone(), kr, vr))
+
+        if not captured or wait is not nothing:
+            for i in range(steps):
+                step(i)
+        else:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                for i in range(steps):
+                    step(i)
+            graph.replay()
+        torch.cuda.synchronize()
+        return data, outs
+
+    def nothing():
+        pass
+
+    (d0, o0), (d1, o1) = run(torch.cuda.synchronize), run(nothing)
+    assert torch.equal(d0, d1)
+    for x, y in zip(o0, o1):
+        assert all(torch.equal(a, b) for a, b in zip(x, y))
+
+
 def test_two_streams_at_once():
     """Calls on two streams, each with a workspace of its own, many of them in flight."""
     D, G, bits = 128, 64, 4

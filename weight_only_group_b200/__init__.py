@@ -639,7 +639,7 @@ def _kv(cache, table, lens, D: int, G: int, bits: int):
     dev = cache.get_device()
     tp, lp = _need_index(table, "table", dev, 2), _need_index(lens, "lens", dev, 1)
     batch, width = table.shape
-    if len(lens) != batch:
+    if lens.shape[0] != batch:
         raise ValueError("table and lens disagree on the number of sequences")
     pages, heads, page_size, held = cache.shape
     tb = 2 * (D * bits // 8) + 8 * (D // G) if G > 0 else 0  # aq_kv_token_bytes, of a form that the call itself checks
@@ -650,22 +650,19 @@ def _kv(cache, table, lens, D: int, G: int, bits: int):
     return _KVCache(cache.data_ptr(), pages, heads, page_size, D, G, bits, tp, lp, batch, width), dev
 
 
-def _need_rows(t, name: str, dev: int, shape) -> None:
-    """bf16 of this shape, strided, its last dimension contiguous."""
+def _need_rows(t, name: str, dev: int, shape):
+    """bf16 of this shape, strided, its last dimension contiguous -> its strides; a dimension of one entry has none that
+    counts."""
     if not isinstance(t, _Tensor) or t.dtype is not _BF16:
         raise TypeError(f"{name} must be a bfloat16 tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the cache's device")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    if t.stride(-1) != 1 and shape[-1] > 1:
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-
-
-def _steps(t):
-    """Strides; a dimension of one entry has none that counts."""
-    st, sh = t.stride(), t.shape
-    return st if 1 not in sh else tuple(0 if n == 1 else s for s, n in zip(st, sh))
+    return st if 1 not in shape else tuple(0 if n == 1 else s for s, n in zip(st, shape))
 
 
 def _need_offsets(offsets, dev: int, batch: int, rows: int) -> int:
@@ -674,7 +671,7 @@ def _need_offsets(offsets, dev: int, batch: int, rows: int) -> int:
             raise ValueError("without offsets every sequence has as many rows: rows must be a multiple of the batch")
         return 0
     p = _need_index(offsets, "offsets", dev, 1)
-    if len(offsets) != batch + 1:
+    if offsets.shape[0] != batch + 1:
         raise ValueError("offsets must have one entry more than there are sequences")
     return p
 
@@ -703,12 +700,10 @@ def aq_kv_append(cache, k, v, table, lens, G: int, bits: int, offsets: torch.Ten
     c, dev = _kv(cache, table, lens, D, G, bits)
     if heads != c.heads:
         raise ValueError(f"k must have the cache's {c.heads} heads")
-    _need_rows(k, "k", dev, shape)
-    _need_rows(v, "v", dev, shape)
+    ks, vs = _need_rows(k, "k", dev, shape), _need_rows(v, "v", dev, shape)
     off = _need_offsets(offsets, dev, c.batch, rows)
     if rows == 0:
         return
-    ks, vs = _steps(k), _steps(v)
     _call((_lib or lib()).aq_kv_append, "aq_kv_append", dev, c, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
           rows, off)
 
@@ -756,7 +751,7 @@ def aq_kv_attention(q, cache, table, lens, G: int, bits: int, scale: float | Non
     batch = c.batch
     if shape[0] != batch:
         raise ValueError(f"q must have a row for each of {batch} sequences")
-    _need_rows(q, "q", dev, shape)
+    st = _need_rows(q, "q", dev, shape)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
@@ -776,7 +771,6 @@ def aq_kv_attention(q, cache, table, lens, G: int, bits: int, scale: float | Non
         workspace = cache.new_empty((L.aq_kv_attention_workspace_bytes(c, tokens, q_heads, window),))
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    st = _steps(q)
     _call(L.aq_kv_attention, "aq_kv_attention", dev, c, q.data_ptr(), tokens, q_heads, st[0],
           st[1] if len(st) == 4 else 0, st[-2], D**-0.5 if scale is None else scale, window, out.data_ptr(), lp,
           workspace.data_ptr(), workspace.numel() * workspace.element_size())

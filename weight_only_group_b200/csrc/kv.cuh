@@ -33,6 +33,34 @@ struct Cache {
   int page_shift;        // log2(page_size)
 };
 
+// The kernels of the cache follow one another in a decode step, each short, so they are launched as programmatic
+// dependents: a kernel's blocks may come up while the one before it in the stream still runs, and wait for its end (and
+// its writes) before they touch memory.  Every thread calls this first.  What they read may thus have been written during
+// their own grid's life, so it is read with plain loads, never the read-only path; and the next kernel is let in only
+// when the wait is over, so at most one is ahead of its inputs.
+AQ_DEVICE void await_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class T>
+AQ_DEVICE T load(const void *p) {
+  return *static_cast<const T *>(p);
+}
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The tile of position `pos` in page `page` of head `h`.
 AQ_DEVICE int64_t tile_index(const Cache &c, int page, int h, int pos) {
   const int in_page = pos & ((1 << c.page_shift) - 1);

@@ -126,7 +126,7 @@ struct Span {
 template <int CHUNK>
 AQ_DEVICE Span span_of(const AttentionArgs &a, int seq) {
   Span x;
-  x.len = max(0, __ldg(a.c.lens + seq));
+  x.len = max(0, load<int32_t>(a.c.lens + seq));
   x.begin = begin_of(a, x.len - a.tokens);
   x.first = x.begin / CHUNK;
   x.chunks = max(1, (min(x.len, cap_of(a)) + CHUNK - 1) / CHUNK - x.first);
@@ -232,10 +232,10 @@ AQ_DEVICE void load_queries(Queries<BITS, D, G, ROWS> &x, const AttentionArgs &a
         const uint16_t *p = q + gi * G + (t * Q::kKW + w) * Q::kPW;
         uint32_t(&v)[Q::kPW / 2] = x.raw[nt][gi][w];
         if constexpr (Q::kPW == 8) {
-          const uint4 u = mine ? ldg_nc16(p) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 u = mine ? load<uint4>(p) : make_uint4(0u, 0u, 0u, 0u);
           v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
         } else {
-          const uint2 u = mine ? ldg_nc8(p) : make_uint2(0u, 0u);
+          const uint2 u = mine ? load<uint2>(p) : make_uint2(0u, 0u);
           v[0] = u.x, v[1] = u.y;
         }
       }
@@ -765,13 +765,13 @@ __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D
   __shared__ int head_unit[kWarps], tail_unit[kWarps], tail_end[kWarps];
   __shared__ bool tail_starts[kWarps];
   __shared__ volatile int abort_flag;
-  asm volatile("griddepcontrol.launch_dependents;");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) {
     for (int i = 0; i < F::kStages; ++i) mbar_init(&bars[warp][i], 1);
     fence_barrier_init();
   }
   if (threadIdx.x == 0) abort_flag = 0;
+  await_previous();
   const int units = a.c.heads * plan.row_tiles;  // of a sequence
   Cursor<CHUNK> cur;
   int begin, end, share;  // the warp's run, in places of the list; places of a warp
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D
       // (only tiles that some row sees: entries in front of a window may hold anything)
       const int e = pos_in >> a.c.page_shift;
       needed = lane < CT && pos_in < ahead.span.len && e < a.c.width && pos_in + kTile > ahead.span.begin;
-      if (needed) page = __ldg(a.c.table + int64_t(ahead.seq) * a.c.width + e);
+      if (needed) page = load<int32_t>(a.c.table + int64_t(ahead.seq) * a.c.width + e);
     };
     auto issue = [&]() {
       const bool there = needed && static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.pages);
@@ -985,7 +985,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   __shared__ float weights[MOST], red[2][kWarps];
   __shared__ float4 sums[SHARES][COLS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = blockIdx.y, cta = blockIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  await_previous();
   const Loose x = plan.loose[cta];
   if (x.unit < 0) return;
   const int units = a.c.heads * plan.row_tiles;
@@ -1094,19 +1094,9 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
   plan.parts = reinterpret_cast<float *>(ws + s.parts);
   plan.heads = reinterpret_cast<float *>(ws + s.heads);
   plan.loose = reinterpret_cast<Loose *>(ws + s.loose);
-  kern<<<s.ctas, F::kThreads, kBytes, stream>>>(a, plan);
-  if ((e = cudaGetLastError()) != cudaSuccess || s.direct || s.ctas == 1) return e;
-  // The join starts while the last CTAs run, and waits for them.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(s.ctas, ROWS);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, ROWS>, a, plan);
+  e = launch_dependent(kern, dim3(s.ctas), F::kThreads, kBytes, stream, a, plan);
+  if (e != cudaSuccess || s.direct || s.ctas == 1) return e;
+  return launch_dependent(join_kernel<D, ROWS>, dim3(s.ctas, ROWS), kJoinThreads, 0, stream, a, plan);
 }
 
 // Calls run for a form: as many rows as a KV head has, up to 16; 8 where the accumulators of 16 rows do not fit a thread's

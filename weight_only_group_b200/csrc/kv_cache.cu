@@ -33,20 +33,20 @@ AQ_DEVICE bool locate(const Cache &c, const int32_t *offsets, int rows_per_seq, 
     int lo = 0, n = c.batch;
     while (n > 1) {
       const int step = (n + 31) >> 5, at = lane * step;
-      const uint32_t below = __ballot_sync(0xffffffffu, at < n && __ldg(offsets + lo + at) <= r) | 1u;
+      const uint32_t below = __ballot_sync(0xffffffffu, at < n && load<int32_t>(offsets + lo + at) <= r) | 1u;
       const int k = 31 - __clz(below);
       lo += k * step;
       n = min(step, n - k * step);
     }
     seq = lo;
-    const int begin = __ldg(offsets + lo);
-    end = __ldg(offsets + lo + 1);
+    const int begin = load<int32_t>(offsets + lo);
+    end = load<int32_t>(offsets + lo + 1);
     if (r < begin || r >= end) return false;
   } else {
     seq = r / rows_per_seq;
     end = (seq + 1) * rows_per_seq;
   }
-  pos = static_cast<int>(max(int64_t(-1), int64_t(__ldg(c.lens + seq)) - end + r));
+  pos = static_cast<int>(max(int64_t(-1), int64_t(load<int32_t>(c.lens + seq)) - end + r));
   return true;
 }
 
@@ -54,7 +54,7 @@ AQ_DEVICE bool locate(const Cache &c, const int32_t *offsets, int rows_per_seq, 
 AQ_DEVICE int page_of(const Cache &c, int seq, int pos) {
   const int i = pos >> c.page_shift;
   if (i >= c.width) return -1;
-  const int page = __ldg(c.table + int64_t(seq) * c.width + i);
+  const int page = load<int32_t>(c.table + int64_t(seq) * c.width + i);
   return page < c.pages ? page : -1;  // (a negative entry stays negative)
 }
 
@@ -68,12 +68,12 @@ struct Bf16x16 {
 AQ_DEVICE Bf16x16 load16(const uint16_t *p, bool wide) {
   Bf16x16 x;
   if (wide) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]),
                    "=r"(x.w[7])
                  : "l"(p));
   } else {
-    const uint4 a = ldg_nc16(p), b = ldg_nc16(p + 8);
+    const uint4 a = load<uint4>(p), b = load<uint4>(p + 8);
     x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w, x.w[4] = b.x, x.w[5] = b.y, x.w[6] = b.z, x.w[7] = b.w;
   }
   return x;
@@ -167,6 +167,7 @@ AQ_DEVICE __half2 encode(const uint32_t (&w)[8], uint32_t (&out)[BITS / 2]) {
 template <int BITS, int G>
 __global__ void __launch_bounds__(kRowsPerBlock * 32) append_kernel(const __grid_constant__ AppendArgs a, int log_lanes) {
   constexpr int GL = G / kVals;  // lanes of a group
+  await_previous();
   const int D = kVals << log_lanes, lane = threadIdx.x & 31, heads_at_once = 32 >> log_lanes;
   const Cache &c = a.c;
   const int l = lane & ((1 << log_lanes) - 1);
@@ -247,6 +248,7 @@ AQ_DEVICE uint4 decode(uint2 w, uint32_t sb) {
 template <int BITS, int G>
 __global__ void __launch_bounds__(kRowsPerBlock * 32) read_kernel(const __grid_constant__ ReadArgs a, int log_lanes) {
   constexpr int GL = G / kVals;
+  await_previous();
   const int D = kVals << log_lanes, lane = threadIdx.x & 31, heads_at_once = 32 >> log_lanes;
   const Cache &c = a.c;
   Place p;
@@ -274,14 +276,14 @@ __global__ void __launch_bounds__(kRowsPerBlock * 32) read_kernel(const __grid_c
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       if constexpr (BITS == 4) {
-        const uint2 x = ldg_nc8(codes + which * v_codes);
+        const uint2 x = load<uint2>(codes + which * v_codes);
         w[which] = make_uint4(x.x, x.y, 0u, 0u);
       } else {
-        w[which] = ldg_nc16(codes + which * v_codes);
+        w[which] = load<uint4>(codes + which * v_codes);
       }
     }
-    sb[0] = ldg_nc4(meta);
-    sb[1] = ldg_nc4(meta + v_meta);
+    sb[0] = load<uint32_t>(meta);
+    sb[1] = load<uint32_t>(meta + v_meta);
     codes += head_step;
     meta += head_step;
   };
@@ -338,16 +340,14 @@ dim3 grid_for(int64_t rows, int heads, int D) {
 template <int BITS, int G>
 struct Append {
   static cudaError_t run(const AppendArgs &a, int D, cudaStream_t s) {
-    append_kernel<BITS, G><<<grid_for(a.rows, a.c.heads, D), kRowsPerBlock * 32, 0, s>>>(a, log_lanes(D));
-    return cudaGetLastError();
+    return launch_dependent(append_kernel<BITS, G>, grid_for(a.rows, a.c.heads, D), kRowsPerBlock * 32, 0, s, a, log_lanes(D));
   }
 };
 
 template <int BITS, int G>
 struct Read {
   static cudaError_t run(const ReadArgs &a, int D, cudaStream_t s) {
-    read_kernel<BITS, G><<<grid_for(a.rows, a.c.heads, D), kRowsPerBlock * 32, 0, s>>>(a, log_lanes(D));
-    return cudaGetLastError();
+    return launch_dependent(read_kernel<BITS, G>, grid_for(a.rows, a.c.heads, D), kRowsPerBlock * 32, 0, s, a, log_lanes(D));
   }
 };
 
