@@ -107,12 +107,13 @@ def attention(c: Cache, q_bits, scale: float, window: int = 0):
     """q_bits: bf16 patterns [batch, tokens, q_heads, D] -> a dict of 64-bit arrays:
 
     out [.., D] and lse [..], the attention; and for bounds of rounding errors
-    spread [.., D] = sum_t w_t scale_t code_td, size [.., D] = sum_t w_t |v_td| (w: the softmax weights), and
-    terms [..] = max_t |scale| sum_d |q_d| (scale_t code_td + |bias_t|), the size of what a score is summed from."""
+    spread [.., D] = sum_t w_t scale_t code_td, size [.., D] = sum_t w_t |v_td| (w: the softmax weights),
+    terms [..] = max_t |scale| sum_d |q_d| (scale_t code_td + |bias_t|), the size of what a score is summed from, and
+    least [..] = n max scale_t max code over V of the n positions that any of the sequence's tokens sees."""
     q = f32(q_bits).astype(np.float64)
     B, n, hq, D = q.shape
     out, spread, size = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
-    lse, terms = np.full(q.shape[:3], -np.inf), np.zeros(q.shape[:3])
+    lse, terms, least = np.full(q.shape[:3], -np.inf), np.zeros(q.shape[:3]), np.zeros(q.shape[:3])
     rep = hq // c.heads
     for b in range(B):
         length = int(c.lens[b])
@@ -123,6 +124,7 @@ def attention(c: Cache, q_bits, scale: float, window: int = 0):
                 continue
             k, v = ([np.stack(x) for x in zip(*(_fields(c, b, p, h, which) for p in known))] for which in (0, 1))
             kx, vx = k[0] * k[1] + k[2], v[0] * v[1] + v[2]
+            least[b, :, h * rep:(h + 1) * rep] = len(known) * max(v[1].max(), 2.0**-15) * (2**c.bits - 1)
             pos = np.array(known)
             for j in range(n):
                 p = length - n + j
@@ -139,7 +141,7 @@ def attention(c: Cache, q_bits, scale: float, window: int = 0):
                     spread[b, j, i] = w @ (v[0] * v[1])[see]
                     size[b, j, i] = w @ np.abs(vx[see])
                     terms[b, j, i] = abs(scale) * ((k[0] * k[1] + np.abs(k[2]))[see] @ np.abs(q[b, j, i])).max()
-    return dict(out=out, lse=lse, spread=spread, size=size, terms=terms)
+    return dict(out=out, lse=lse, spread=spread, size=size, terms=terms, least=least)
 
 
 def attention_bounds(r: dict, D: int):
@@ -149,9 +151,14 @@ def attention_bounds(r: dict, D: int):
     sum's size; with the factor, the maximum's subtraction and exp2 that makes an absolute error of at most
     e = (D + 16) 2^-23 terms + 2^-21, so a weight is off by a factor of 1 +- 2e (its own and the sum's).  A weight's product
     with a V scale rounds to fp16 (2^-11), the sums over tokens are in fp32 (2^-23 for each of the at most 2^11 joined
-    partial sums and accumulations that follow one another: 2^-12), and the result rounds to bf16 (2^-8)."""
+    partial sums and accumulations that follow one another: 2^-12), and the result rounds to bf16 (2^-8).
+
+    Where the rounded product is subnormal its error is absolute instead, half a unit, 2^-25.  It stands for
+    2^(x - m) s with m = M + e - 13, M at most the row's maximum and 2^e at most twice the largest scale s of V (or 2^-14),
+    and the result is divided by the sum of 2^(x - m), which is at least 2^(13 - e).  So a token's code adds an error of at most
+    2^-25 2^(e - 13) code = 2^-38 2^e code <= 2^-37 max(s, 2^-15) code, and n tokens at most 2^-37 least."""
     e = ((D + 16) * 2.0**-23 * r["terms"] + 2.0**-21)[..., None]
-    off = (2.0**-11 + 2.0**-12) * r["spread"] + (2 * e + 2.0**-12) * r["size"]
+    off = (2.0**-11 + 2.0**-12) * r["spread"] + (2 * e + 2.0**-12) * r["size"] + 2.0**-37 * r["least"][..., None]
     with np.errstate(invalid="ignore"):
         lse = e[..., 0] + 2.0**-21 * (np.where(np.isfinite(r["lse"]), np.abs(r["lse"]), 0.0) + 1.0)
     return 2.0**-8 * np.abs(r["out"]) + (1 + 2.0**-8) * off + 2.0**-133, lse

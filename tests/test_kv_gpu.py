@@ -268,6 +268,37 @@ def test_attention_scales(scale):
     _attend(c, queries(2, 1, 6, 64, 52), scale=scale)
 
 
+@pytest.mark.parametrize("tokens,q_heads", [(1, 3), (2, 6)])
+@pytest.mark.parametrize("bad", (float("nan"), float("inf"), -float("inf")))
+def test_attention_beside_a_query_that_is_not_finite(tokens, q_heads, bad):
+    c = filled([50, 9], heads=1, page_size=16, D=64, G=32, bits=4, seed=53)
+    gpu, q = on_gpu(c), to_gpu(queries(2, tokens, q_heads, 64, 54))
+    want = aq.aq_kv_attention(q, *gpu, 32, 4)
+    q[0, 0, 1, 7] = bad
+    got = aq.aq_kv_attention(q, *gpu, 32, 4)
+    assert not torch.isfinite(got[0, 0, 1]).all()
+    want[0, 0, 1] = got[0, 0, 1] = 0
+    assert torch.equal(got, want)
+
+
+def test_attention_of_queries_of_extreme_sizes():
+    """Queries of 2^-120 to 2^90 against keys that bring the scores back to where a softmax is neither flat nor sharp."""
+    D, G, bits = 64, 32, 8
+    rng = np.random.default_rng(8)
+    q, sizes = rng.standard_normal((1, 1, 6, D)), 2.0 ** np.array([-120, -60, -14, 0, 12, 14])
+    c = cache([70], heads=6, page_size=16, D=D, G=G, bits=bits, seed=55)
+    k = rng.standard_normal((70, 6, D)) / np.clip(sizes, 2.0**-13, None)[None, :, None]
+    ref.append(c, bf16_bits(k), rows(70, 6, D, 56), [0, 70])
+    _attend(c, bf16_bits(q * sizes[None, None, :, None]))
+
+
+def test_attention_of_many_tokens():
+    """As many new tokens as a short prompt has: a triangle of masks."""
+    c = filled([130, 90, 7], heads=1, page_size=32, D=64, G=64, bits=4, seed=57)
+    _attend(c, queries(3, 90, 2, 64, 58))
+    _attend(c, queries(3, 90, 2, 64, 59), window=20)
+
+
 def test_attention_sharp_and_flat():
     """Scores far apart, the largest of them first, last and in between; q of very different sizes, and zero."""
     lens = [400, 400, 400, 400]

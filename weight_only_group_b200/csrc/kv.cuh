@@ -58,7 +58,9 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) cudaGetLastError();  // (reported to the caller here, not to whoever asks next)
+  return e;
 }
 
 // The tile of position `pos` in page `page` of head `h`.

@@ -451,10 +451,11 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
       }
     partly = __any_sync(0xffffffffu, partly);
   }
-  // --- the running reference m of a row.  A weight is 2^(x - m), m = (a maximum so far) + e - 11, where V scales so far are
-  // below 2^e.  m stands while no weight times scale can pass 2^15: scores at most 2^4 above the maximum it was taken from,
-  // scales below 2^e.  So a look at this lane's own values is enough but for the first chunks and the rare new extreme.
-  // (weight * scale) is a normal fp16 down to 2^-25 of the largest, and rounds to nothing below a 2^-36th of it.
+  // --- the running reference m of a row.  A weight is 2^(x - m), m = (a maximum so far) + e - 13, where V scales so far are
+  // at most 2^e (1 - 2^-11).  m stands while no weight times scale can pass fp16's 65504 = 2^16 (1 - 2^-11): scores at most 3
+  // (a factor of 8) above the maximum it was taken from, scales within 2^e.  So a look at this lane's own values is enough
+  // but for the first chunks and the rare new extreme.  (weight * scale) is a normal fp16 down to 2^-27 of the largest, and
+  // below that its error is at most half a subnormal's unit, a 2^-38th of it.
   __half2 top = __half2half2(__ushort_as_half(0));  // (scale, bias): the low half is what counts; a NaN is passed over
 #pragma unroll
   for (int i = 0; i < CT; ++i)
@@ -473,7 +474,7 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
 #pragma unroll
       for (int i = 1; i < CT; ++i) v = fmaxf(v, fmaxf(x[i][nt][0][c], x[i][nt][1][c]));
       mx[nt][c] = v;
-      more |= fmaf(v, st.rs[nt][c], static_cast<float>(st.e - 15)) > st.m[nt][c];
+      more |= fmaf(v, st.rs[nt][c], static_cast<float>(st.e - 16)) > st.m[nt][c];
     }
   if (__any_sync(0xffffffffu, more)) {
     const int e = max(st.e, static_cast<int>(__reduce_max_sync(0xffffffffu, top_bits) >> 10) - 14);
@@ -488,7 +489,7 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        const float mn = fmaxf(st.m[nt][c] + shift, fmaf(v, st.rs[nt][c], static_cast<float>(e - 11)));
+        const float mn = fmaxf(st.m[nt][c] + shift, fmaf(v, st.rs[nt][c], static_cast<float>(e - 13)));
         al[c] = exp2_approx(st.m[nt][c] - mn);
         st.m[nt][c] = mn;
         st.l[nt][c] *= al[c];

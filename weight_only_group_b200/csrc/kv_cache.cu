@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kRowsPerBlock * 32) read_kernel(const __grid_c
   const uint8_t *codes = c.data + tile_index(c, p.page, 0, p.pos) * tile_bytes(D, G, BITS) + h * head_bytes + in * rb + l * (2 * BITS);
   const uint8_t *meta = codes + 2 * kTile * rb + (in * 2 * (D / G) + l / GL) * 4 - (in * rb + l * (2 * BITS));
   const int v_codes = kTile * rb, v_meta = D / G * 4;
-  auto load = [&](uint4(&w)[2], uint32_t(&sb)[2]) {
+  auto fetch = [&](uint4(&w)[2], uint32_t(&sb)[2]) {
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       if constexpr (BITS == 4) {
@@ -291,13 +291,13 @@ __global__ void __launch_bounds__(kRowsPerBlock * 32) read_kernel(const __grid_c
   if (h >= c.heads) return;
   uint4 w[2];
   uint32_t sb[2];
-  load(w, sb);
+  fetch(w, sb);
   while (true) {
     h += stride;
     const bool more = h < c.heads;
     uint4 w1[2];
     uint32_t sb1[2];
-    if (more) load(w1, sb1);
+    if (more) fetch(w1, sb1);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       if constexpr (BITS == 4) {
