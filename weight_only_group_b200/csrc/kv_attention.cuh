@@ -976,10 +976,61 @@ __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D
   if (threadIdx.x == 0 && !plan.direct) plan.loose[blockIdx.x] = loose;
 }
 
-// Joins the units that several CTAs have a part of: block (i, r) takes row r of the one that starts in CTA i's run and
-// goes on behind it.  Threads share the parts (there are up to as many as CTAs) as well as the columns.
+// The join kernels: they join the units that several CTAs have a part of.  The first part of a unit is what CTA `cta` has at
+// its end, the others what the CTAs behind it have at their beginnings.
+template <int PART>
+AQ_DEVICE const float *part_of(const Plan &plan, int cta, int k) {
+  return plan.parts + (int64_t(cta + k) * 2 + (k == 0 ? 1 : 0)) * PART;
+}
+
+// Where units are many, and have few parts each: block i takes the one that starts in CTA i's run and goes on behind it, and a
+// warp a row of it.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttentionArgs a,
+__global__ void __launch_bounds__(kJoinThreads) join_few_kernel(const __grid_constant__ AttentionArgs a,
+                                                                const __grid_constant__ Plan plan) {
+  constexpr int PART = ROWS * (D + 2), COLS = D / 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+  await_previous();
+  const Loose x = plan.loose[cta];
+  if (x.unit < 0) return;
+  const int units = a.c.heads * plan.row_tiles;
+  const int seq = x.unit / units, u = x.unit - seq * units, h = u / plan.row_tiles, row0 = (u - h * plan.row_tiles) * ROWS;
+  const int n = x.last - cta + 1;
+  for (int r = warp; r < ROWS && row0 + r < a.tokens * a.group; r += kJoinThreads / 32) {
+    float m = -1e30f, l = 0.0f;
+    for (int k = lane; k < n; k += 32) m = fmaxf(m, part_of<PART>(plan, cta, k)[r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float4 o[(COLS + 31) / 32] = {};
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      const int mine = min(k0 + lane, n - 1);
+      const float *p = part_of<PART>(plan, cta, mine);
+      const float wk = k0 + lane < n ? exp2_approx(p[r] - m) : 0.0f;
+      l = fmaf(wk, p[ROWS + r], l);
+#pragma unroll 4
+      for (int k = 0; k < min(32, n - k0); ++k) {
+        const float w = __shfl_sync(0xffffffffu, wk, k);
+        const float4 *v = reinterpret_cast<const float4 *>(part_of<PART>(plan, cta, k0 + k) + 2 * ROWS + r * D);
+#pragma unroll
+        for (int c = 0; c < (COLS + 31) / 32; ++c) {
+          const float4 y = COLS >= 32 || lane < COLS ? v[c * 32 + lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          o[c].x = fmaf(w, y.x, o[c].x), o[c].y = fmaf(w, y.y, o[c].y);
+          o[c].z = fmaf(w, y.z, o[c].z), o[c].w = fmaf(w, y.w, o[c].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+#pragma unroll
+    for (int c = 0; c < (COLS + 31) / 32; ++c)
+      if (COLS >= 32 || lane < COLS) put_out<D>(a, seq, h, row0 + r, c * 32 + lane, o[c], m, l);
+  }
+}
+
+// Where units are few and have many parts: block (i, r) takes row r of it, and its threads share the parts (up to as many
+// as there are CTAs) as well as the columns.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) join_many_kernel(const __grid_constant__ AttentionArgs a,
                                                         const __grid_constant__ Plan plan) {
   constexpr int PART = ROWS * (D + 2), COLS = D / 4, kThreads = kJoinThreads, kWarps = kThreads / 32;
   constexpr int SHARES = kThreads / COLS, MOST = kMostCtas * kSms;
@@ -994,8 +1045,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int row = (u - h * plan.row_tiles) * ROWS + r;
   if (row >= a.tokens * a.group) return;
   const int n = x.last - cta + 1;
-  // the first part is what CTA `cta` has at its end, the others what the CTAs behind it have at their beginnings
-  auto part = [&](int k) -> const float * { return plan.parts + (int64_t(cta + k) * 2 + (k == 0 ? 1 : 0)) * PART; };
+  auto part = [&](int k) { return part_of<PART>(plan, cta, k); };
   float m = -1e30f, l = 0.0f, mk[(MOST + kThreads - 1) / kThreads], lk[(MOST + kThreads - 1) / kThreads];
 #pragma unroll
   for (int i = 0; i < (MOST + kThreads - 1) / kThreads; ++i) {
@@ -1097,7 +1147,10 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
   plan.loose = reinterpret_cast<Loose *>(ws + s.loose);
   e = launch_dependent(kern, dim3(s.ctas), F::kThreads, kBytes, stream, a, plan);
   if (e != cudaSuccess || s.direct || s.ctas == 1) return e;
-  return launch_dependent(join_kernel<D, ROWS>, dim3(s.ctas, ROWS), kJoinThreads, 0, stream, a, plan);
+  // (up to eight parts a unit on average: a warp has those of a row on their way at once or twice)
+  if (int64_t(s.ctas) <= 8 * int64_t(a.c.batch) * a.c.heads * s.row_tiles)
+    return launch_dependent(join_few_kernel<D, ROWS>, dim3(s.ctas), kJoinThreads, 0, stream, a, plan);
+  return launch_dependent(join_many_kernel<D, ROWS>, dim3(s.ctas, ROWS), kJoinThreads, 0, stream, a, plan);
 }
 
 // Calls run for a form: as many rows as a KV head has, up to 16; 8 where the accumulators of 16 rows do not fit a thread's
