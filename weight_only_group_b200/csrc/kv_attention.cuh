@@ -527,19 +527,20 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
 #pragma unroll
             for (int gj = gi; gj < gi + GROUPS; ++gj) {
               const float2 sb = pair_of(sv[i][half][gj]);
-              float z[RL];
-#pragma unroll
-              for (int c = 0; c < RL; ++c) {
-                y[F::col(gj, c)] = x[i][nt][half][c] * sb.x;
-                z[c] = x[i][nt][half][c] * sb.y;
-              }
               if (partly) {
 #pragma unroll
-                for (int c = 0; c < RL; ++c)
-                  if (!(seen >> (((i * NT + nt) * 2 + half) * RL + c) & 1)) y[F::col(gj, c)] = z[c] = 0.0f;
-              }
+                for (int c = 0; c < RL; ++c) {
+                  const bool see = seen >> (((i * NT + nt) * 2 + half) * RL + c) & 1;
+                  y[F::col(gj, c)] = see ? x[i][nt][half][c] * sb.x : 0.0f;
+                  st.bias[nt][gj][c] += see ? x[i][nt][half][c] * sb.y : 0.0f;
+                }
+              } else {
 #pragma unroll
-              for (int c = 0; c < RL; ++c) st.bias[nt][gj][c] += z[c];
+                for (int c = 0; c < RL; ++c) {
+                  y[F::col(gj, c)] = x[i][nt][half][c] * sb.x;
+                  st.bias[nt][gj][c] = fmaf(x[i][nt][half][c], sb.y, st.bias[nt][gj][c]);
+                }
+              }
             }
             b[nt][half] = transpose8x8(pack_half2(y[0], y[1]));
           }
