@@ -417,39 +417,39 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
       }
     }
   }
-  // --- which tokens a row sees.  What it does not see weighs 2^-infinity = 0, and where a scale or bias might be infinite
-  // or NaN the products are zeroed too: it is where no row sees the token (nothing may have been written there), and it may
-  // be where another row does (seen: bit ((i * NT + nt) * 2 + half) * RL + c; partly: some row sees a token that another
-  // does not)
-  uint32_t seen = 0;
-  bool partly = false;
+  // --- which tokens a row sees.  What it does not see weighs 2^-infinity = 0.  That is not enough where a scale or bias of V
+  // is infinite or NaN, as it may be where no row sees the token (nothing may have been written there) or where another row
+  // does: such pairs go in as zeros, and the sums of weights of the rows that do see the token become NaN.
   if (valid != (1u << CT) - 1u || pos < st.lo_all || pos + kTile * CT > st.hi_all) {
 #pragma unroll
     for (int i = 0; i < CT; ++i)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int at = pos + i * kTile + half * 8 + tok;
-        bool any = false, all = true;
+        bool odd = !(valid >> i & 1);
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+          const uint32_t sb = sv[i][half][gi];
+          odd |= (sb & 0x7C00u) == 0x7C00u || (sb & 0x7C000000u) == 0x7C000000u;
+        }
+        bool any = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < RL; ++c) {
             const int p = st.pos[nt][c];
             const bool see = (valid >> i & 1) && at >= begin_of(a, p) && at < end_of(a, p);
-            if (see) seen |= 1u << (((i * NT + nt) * 2 + half) * RL + c);
-            else x[i][nt][half][c] = -CUDART_INF_F;
+            if (!see) x[i][nt][half][c] = -CUDART_INF_F;
+            else if (odd) st.l[nt][c] = CUDART_NAN_F;
             any |= see;
-            all &= see;
           }
-        // (the four lanes of a token hold different rows: what any of them sees counts)
+        // (the four lanes of a token hold different rows: what any of them sees counts, for its scales enter the reference)
         any = __ballot_sync(0xffffffffu, any) >> (lane & 28) & 15u;
-        partly |= any && !all;
-        if (!any) {
+        if (odd || !any) {
 #pragma unroll
           for (int gi = 0; gi < NG; ++gi) sv[i][half][gi] = 0;
         }
       }
-    partly = __any_sync(0xffffffffu, partly);
   }
   // --- the running reference m of a row.  A weight is 2^(x - m), m = (a maximum so far) + e - 13, where V scales so far are
   // at most 2^e (1 - 2^-11).  m stands while no weight times scale can pass fp16's 65504 = 2^16 (1 - 2^-11): scores at most 3
@@ -527,19 +527,10 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
 #pragma unroll
             for (int gj = gi; gj < gi + GROUPS; ++gj) {
               const float2 sb = pair_of(sv[i][half][gj]);
-              if (partly) {
 #pragma unroll
-                for (int c = 0; c < RL; ++c) {
-                  const bool see = seen >> (((i * NT + nt) * 2 + half) * RL + c) & 1;
-                  y[F::col(gj, c)] = see ? x[i][nt][half][c] * sb.x : 0.0f;
-                  st.bias[nt][gj][c] += see ? x[i][nt][half][c] * sb.y : 0.0f;
-                }
-              } else {
-#pragma unroll
-                for (int c = 0; c < RL; ++c) {
-                  y[F::col(gj, c)] = x[i][nt][half][c] * sb.x;
-                  st.bias[nt][gj][c] = fmaf(x[i][nt][half][c], sb.y, st.bias[nt][gj][c]);
-                }
+              for (int c = 0; c < RL; ++c) {
+                y[F::col(gj, c)] = x[i][nt][half][c] * sb.x;
+                st.bias[nt][gj][c] = fmaf(x[i][nt][half][c], sb.y, st.bias[nt][gj][c]);
               }
             }
             b[nt][half] = transpose8x8(pack_half2(y[0], y[1]));
@@ -614,7 +605,7 @@ AQ_DEVICE int64_t out_row(const AttentionArgs &a, int seq, int h, int r) {
 }
 
 AQ_DEVICE float log_sum(float m, float l) {
-  return l > 0.0f ? (m + __log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+  return l == 0.0f ? -CUDART_INF_F : (m + __log2f(l)) * CUDART_LN2_F;
 }
 
 template <int BITS, int D, int G, int ROWS>
