@@ -116,7 +116,7 @@ static aq_status check_attention(const aq_kv_cache *cache, int64_t tokens, int64
   // units of work (a chunk of a sequence for each head and each eight rows or fewer) and query rows are counted in 32 bits
   if (cache->batch > 0) {
     const double rows = double(cache->batch) * double(tokens) * double(q_heads);
-    const double chunks = double(cache->width) * cache->page_size / aq::kv::kTile + 1.0;
+    const double chunks = double(cache->width) * cache->page_size / aq::kv::kTile + 8.0;  // (and what a unit costs)
     if (rows > 2e9 || double(cache->batch) * double(cache->heads) * chunks > 1e9 || rows / 8 * chunks > 1e9)
       return AQ_ERR_UNSUPPORTED;
   }

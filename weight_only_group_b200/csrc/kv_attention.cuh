@@ -78,6 +78,10 @@ struct Form {
   // two-tile stages would leave no room for three stages.
   static constexpr int kCT = kTileBytes > 4800 ? 1 : 2;
   static constexpr int kStage = kCT * kTileBytes;
+  // Places in the list of chunks that a unit takes in front of its first: what reading its queries and writing its result
+  // takes a warp, in chunks.  Measured with chunks of 32 tokens, for 0 to 3: 64 ragged sequences, four rows 72.5, 65.1, 64.1 and
+  // 66.2 us, eight rows 95.0, 80.0, 76.7 and 75.1; 200 sequences of up to 400 tokens, four rows 27.8, 26.3, 24.2 and 25.4.
+  static constexpr int kUnitCost = (ROWS > 4 ? 3 : 2) * (2 / kCT);
   static constexpr int kPart = ROWS * (D + 2);       // floats of a partial result: max, sum, accumulator
   // Warps of a CTA and CTAs of an SM: 16 warps of 128 registers for four rows, 12 of 168 for eight, whose accumulators and
   // queries take 24 more, and 8 of 255 where an accumulator, or a ring of three stages, leaves no room for more.  Measured:
@@ -728,10 +732,6 @@ AQ_DEVICE void put_out(const AttentionArgs &a, int seq, int h, int r, int c, flo
 }
 
 // A warp's place in the list of chunks: units are numbered sequence by sequence, heads and then row tiles within one.
-// A unit counts kUnitCost chunks more than it has, in front of its first: reading its queries and writing its result take
-// a warp about as long as a chunk of 32 tokens (2 us beside 2.3 us with all SMs busy).
-constexpr int kUnitCost = 1;
-
 template <int CHUNK>
 struct Cursor {
   int seq, head, row_tile;
@@ -751,7 +751,7 @@ template <int BITS, int D, int G, int ROWS>
 __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D, G, ROWS>::kCtas)
     attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Plan plan) {
   using F = Form<BITS, D, G, ROWS>;
-  constexpr int CT = F::kCT, CHUNK = CT * kTile, kWarps = F::kWarps, kThreads = F::kThreads;
+  constexpr int CT = F::kCT, CHUNK = CT * kTile, kWarps = F::kWarps, kThreads = F::kThreads, kUnitCost = F::kUnitCost;
   extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings
   __shared__ uint64_t bars[kWarps][F::kStages];
   __shared__ int sums[kThreads + 1], warp_sums[kWarps];
@@ -1096,7 +1096,7 @@ struct Sizes {
 template <int BITS, int D, int G, int ROWS>
 Sizes sizes_of(const AttentionArgs &a) {
   using F = Form<BITS, D, G, ROWS>;
-  constexpr int kWarps = F::kWarps;
+  constexpr int kWarps = F::kWarps, kUnitCost = F::kUnitCost;
   Sizes s;
   s.row_tiles = (a.tokens * a.group + ROWS - 1) / ROWS;
   const int64_t units = int64_t(a.c.batch) * a.c.heads * s.row_tiles, slots = int64_t(kSms) * F::kCtas;
