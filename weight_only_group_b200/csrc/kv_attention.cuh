@@ -83,20 +83,22 @@ struct Form {
   // 66.2 us, eight rows 95.0, 80.0, 76.7 and 75.1; 200 sequences of up to 400 tokens, four rows 27.8, 26.3, 24.2 and 25.4.
   static constexpr int kUnitCost = (ROWS > 4 ? 3 : 2) * (2 / kCT);
   static constexpr int kPart = ROWS * (D + 2);       // floats of a partial result: max, sum, accumulator
-  // Warps of a CTA and CTAs of an SM: 16 warps of 128 registers for four rows, 12 of 168 for eight, whose accumulators and
-  // queries take 24 more, and 8 of 255 where an accumulator, or a ring of three stages, leaves no room for more.  Measured:
-  // 64 ragged sequences, 4 bits, four rows 68.3 us at 16 warps and 71.7 at 12; eight rows 87.7 and 86.4 (up to 1500 tokens
-  // 32.5 and 27.9); 8 bits and D = 128, 32 sequences, eight rows 120 us at 8 warps, 122 at 12 and 128 at 16 (these two with
-  // chunks of one tile).
-  static constexpr int kSmem = 224 * 1024;
-  static constexpr bool kSmall = D <= 128 && kSmem / (12 * kStage) >= 3;
-  static constexpr int kWarps = kSmall && ROWS == 8 ? 4 : 8;
-  static constexpr int kCtas = !kSmall || ROWS == 16 ? 1 : ROWS == 8 ? 3 : 2;
+  // Two stages for each warp.  Measured against three: 64 ragged sequences, 4 bits, four rows 63.3 and 64.2 us, eight rows 73.1
+  // and 75.2; 32 sequences, 8 bits 113.9 and 117.5 us: what is in flight over an SM is enough, and the rest is left to L1.
+  static constexpr int kStages = 2;
+  static constexpr int kRing = kStages * kStage;  // bytes of a warp's ring
+  // Warps of a CTA and CTAs of an SM.  Four rows: 16 warps of 128 registers.  Eight rows, whose accumulators and queries take
+  // 24 more: 12 warps of 168.  8 warps of 255 where 16 rows' or wide heads' accumulators leave no room for more, and for
+  // the tiles of 8 bits at D = 128, of which 8 warps keep enough in flight.  Measured: ragged, four rows 68.3 us at 16 warps and
+  // 71.7 at 12; eight rows 80.2 at 16 and 75.2 at 12; 16 rows 107.9 in CTAs of 8 warps and 105.5 in CTAs of 4; 8 bits, D = 128,
+  // eight rows 113.3 at 8 warps and 124.5 at 12.
+  static constexpr bool kSmall = D <= 128 && kStage <= 6144;
+  static constexpr int kWarps = ROWS == 4 ? 8 : 4;
+  static constexpr int kCtas = ROWS == 4 ? (kSmall ? 2 : 1) : kSmall && ROWS == 8 ? 3 : 2;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStages = kSmem / kCtas / (kWarps * kStage) > 4 ? 4 : kSmem / kCtas / (kWarps * kStage);
-  static constexpr int kRing = kStages * kStage;     // bytes of a warp's ring
-  static_assert(kStages >= 2 && kRing >= kPart * 4, "a warp's ring holds two stages, and its last partial result");
-  static_assert(kCtas <= kMostCtas, "the join kernel's room for parts");
+  static_assert(kRing >= kPart * 4, "a warp's ring holds its last partial result");
+  static_assert(kCtas * (kWarps * kRing + 4 * 1024) <= 228 * 1024, "the CTAs of an SM share its memory");
+  static_assert(kCtas <= kMostCtas, "the join kernels' room for parts");
 };
 
 // What a CTA leaves for the join: the unit that starts in its run and goes on
