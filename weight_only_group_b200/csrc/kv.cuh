@@ -1,5 +1,5 @@
 // The paged, group-wise quantised key-value cache: its layout and the argument
-// blocks of its kernels (kv_cache.cu writes and reads it, kv_attention.cuhh
+// blocks of its kernels (kv_cache.cu writes and reads it, kv_attention.cuh
 // attends to it).
 //
 // Layout of the cache: page_size * token_bytes bytes for each of [pages, heads].  A page of
@@ -16,6 +16,9 @@ namespace aq {
 namespace kv {
 
 constexpr int kTile = 16;  // tokens of a tile
+
+// Fault bits that these kernels raise: kFaultBadIndex for a page outside the cache or a position outside the table (zero
+// rows, or the tokens left out), kFaultQmvWait where attention gave up waiting for a tile.
 
 __host__ __device__ constexpr int row_bytes(int D, int bits) { return D * bits / 8; }
 __host__ __device__ constexpr int meta_bytes(int D, int G) { return 8 * (D / G); }

@@ -12,8 +12,8 @@
 // converted.  The nibble above counts 16 times, which q's fragment (K) and the
 // accumulator's rows (V) take back, both exactly.
 //
-// Bound: the cache's bytes, each read once.  A KV head's few query rows (8 or 16
-// at a time) make mma.sync m16n8k16 the right size: tokens (K) or dimensions (V)
+// Bound: the cache's bytes, each read once.  A KV head's few query rows (4, 8 or
+// 16 at a time) make mma.sync m16n8k16 the right size: tokens (K) or dimensions (V)
 // are its 16 rows, query rows its 8 columns.  A tcgen05 tile has 128 rows or more
 // and takes its operands from shared or tensor memory, so each code would be
 // unpacked into memory once more for work that is a few percent of the pipe.
@@ -22,11 +22,11 @@
 // kCT tiles of 16 tokens) are counted, heads and row tiles included, and every
 // warp of the grid takes an equal run of them, whatever sequences it spans.  A
 // warp streams its run through a ring of its own (one bulk copy for each tile,
-// which lies in one piece, lane 0 issuing), keeps a running maximum, sum and
+// which lies in one piece), keeps a running maximum, sum and
 // accumulator in registers, and never waits for another warp until its run is
 // done.  Units (a sequence's KV head and row tile) that a run holds whole are
 // written out at once; what is left of a warp's run at its two ends is joined in
-// the CTA, and what is left of the CTA's run at its two ends by the join kernel,
+// the CTA, and what is left of the CTA's run at its two ends by a second kernel,
 // always in the order of the tokens, so results repeat bit for bit.
 #pragma once
 
@@ -74,8 +74,8 @@ struct Form {
   static __host__ __device__ constexpr bool first_of(int gi) { return !kPair || (gi & 1) == 0; }
   static __host__ __device__ constexpr bool last_of(int gi) { return !kPair || (gi & 1) == 1 || gi == kNG - 1; }
   static __host__ __device__ constexpr int begin_of(int gi) { return kPair ? gi & ~1 : gi; }
-  // Tiles of a chunk: two share a look at the maximum; one where a ring of
-  // two-tile stages would leave no room for three stages.
+  // Tiles of a chunk: two share a look at the maximum; one where two stages of two for each of 8 warps would not fit an SM
+  // (8 bits at D = 256).
   static constexpr int kCT = kTileBytes > 4800 ? 1 : 2;
   static constexpr int kStage = kCT * kTileBytes;
   // Places in the list of chunks that a unit takes in front of its first: what reading its queries and writing its result
