@@ -105,12 +105,13 @@ AQ_DEVICE bool find(const Cache &c, const int32_t *offsets, int rows_per_seq, in
 }
 
 // Codes of 16 values of a group as words, two values an instruction where there is one for two.  The definition's IEEE
-// quotient d / s comes from the correctly rounded reciprocal y of s by Markstein's theorem (P. Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990): with q = rn(d y), which is within an ulp, and the
-// residual r = d - q s, which one fma gives exactly, rn(q + r y) is the correctly rounded quotient.  s is fp16, so nothing
-// here overflows, and where d is so small that r underflows the code is 0 either way.  (A product with y alone would not
-// do: inputs of few bits make exact ties common.)  Adding 1.5 2^23 rounds to an integer, half to even, and leaves it in
-// the low bits; clamping to integers may as well come before.
+// quotient d / s comes from the correctly rounded reciprocal y of s, as in Markstein's theorem (P. Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990): q = rn(d y) is within two units of the last place;
+// the residual r = d - q s is exact in one fma, for s, an fp16, has 11 bits, and r thus at most 13; and rn(q + r y) rounds a
+// number within 2^-45 of the quotient, which itself is 2^-36 or more away from the middle of two fp32, being one of 24 bits
+// by one of 11.  Nothing here overflows, and where d is so small that r underflows the code is 0 either way.  (A product
+// with y alone would not do: inputs of few bits make exact ties common.)  Adding 1.5 2^23 rounds to an integer, half to
+// even, and leaves it in the low bits; clamping to integers may as well come before.
 template <int BITS>
 AQ_DEVICE void encode16(const uint32_t (&w)[8], float sf, float bf, uint32_t (&out)[BITS / 2]) {
   constexpr float qmax = float((1 << BITS) - 1), kMagic = 12582912.0f;
