@@ -525,6 +525,25 @@ def test_steps_that_follow_one_another(captured):
         assert all(torch.equal(a, b) for a, b in zip(x, y))
 
 
+def test_broadcast_inputs_and_drafts_taken_back():
+    """One head's values for all heads and one query for all rows (strides of 0); tokens that a draft wrote are written anew."""
+    D, G, bits, H, Hq = 64, 32, 8, 3, 6
+    c = filled([40, 17], heads=H, page_size=16, D=D, G=G, bits=bits, seed=61, width=4)
+    data, table, ln = on_gpu(c)
+    for new, back, seed in ((3, 2, 62), (2, 0, 63)):
+        c.lens = c.lens + np.int32(new)
+        ln.copy_(torch.from_numpy(c.lens))
+        k, v = rows(2 * new, 1, D, seed), rows(2 * new, 1, D, seed + 10)
+        aq.aq_kv_append(data, to_gpu(k).expand(-1, H, -1), to_gpu(v).expand(-1, H, -1), table, ln, G, bits)
+        ref.append(c, np.repeat(k, H, 1), np.repeat(v, H, 1))
+        assert np.array_equal(data.cpu().numpy(), c.data)
+        q = queries(1, 1, 1, D, seed + 20)
+        got = aq.aq_kv_attention(to_gpu(q).expand(2, new, Hq, D), data, table, ln, G, bits)
+        _check(c, np.broadcast_to(q, (2, new, Hq, D)), got)
+        c.lens = c.lens - np.int32(back)
+    assert aq.aq_device_fault() == 0
+
+
 def test_two_streams_at_once():
     """Calls on two streams, each with a workspace of its own, many of them in flight."""
     D, G, bits = 128, 64, 4
