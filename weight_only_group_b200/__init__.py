@@ -715,7 +715,7 @@ def aq_kv_read(cache, table, lens, rows: int, D: int, G: int, bits: int, offsets
     off = _need_offsets(offsets, dev, c.batch, rows)
     shape = (rows, c.heads, D)
     if out is None:
-        k = torch.empty(shape, dtype=_BF16, device=cache.device)
+        k = cache.new_empty(shape, dtype=_BF16)
         out = (k, torch.empty_like(k))
     else:
         k, v = out
