@@ -982,7 +982,7 @@ AQ_DEVICE const float *part_of(const Plan &plan, int cta, int k) {
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) join_few_kernel(const __grid_constant__ AttentionArgs a,
                                                                 const __grid_constant__ Plan plan) {
-  constexpr int PART = ROWS * (D + 2), COLS = D / 4;
+  constexpr int PART = ROWS * (D + 2), COLS = D / 4, CN = (COLS + 31) / 32, AHEAD = 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   await_previous();
   const Loose x = plan.loose[cta];
@@ -991,32 +991,53 @@ __global__ void __launch_bounds__(kJoinThreads) join_few_kernel(const __grid_con
   const int seq = x.unit / units, u = x.unit - seq * units, h = u / plan.row_tiles, row0 = (u - h * plan.row_tiles) * ROWS;
   const int n = x.last - cta + 1;
   for (int r = warp; r < ROWS && row0 + r < a.tokens * a.group; r += kJoinThreads / 32) {
-    float m = -1e30f, l = 0.0f;
-    for (int k = lane; k < n; k += 32) m = fmaxf(m, part_of<PART>(plan, cta, k)[r]);
+    // a lane looks after the reference and the weights' sum of a part, 32 parts at a time; the columns of the first parts are
+    // asked for before it is known what they weigh
+    float mk = lane < n ? part_of<PART>(plan, cta, lane)[r] : -1e30f, lk = lane < n ? part_of<PART>(plan, cta, lane)[ROWS + r] : 0.0f;
+    auto columns = [&](float4(&y)[CN], int k) {
+      const float4 *v = reinterpret_cast<const float4 *>(part_of<PART>(plan, cta, k) + 2 * ROWS + r * D);
+#pragma unroll
+      for (int c = 0; c < CN; ++c) y[c] = COLS >= 32 || lane < COLS ? v[c * 32 + lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    float4 early[AHEAD][CN];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (k < n) columns(early[k], k);
+    float m = mk, l = 0.0f;
+    for (int k = lane + 32; k < n; k += 32) m = fmaxf(m, part_of<PART>(plan, cta, k)[r]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float4 o[(COLS + 31) / 32] = {};
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      const int mine = min(k0 + lane, n - 1);
-      const float *p = part_of<PART>(plan, cta, mine);
-      const float wk = k0 + lane < n ? exp2_approx(p[r] - m) : 0.0f;
-      l = fmaf(wk, p[ROWS + r], l);
-#pragma unroll 4
-      for (int k = 0; k < min(32, n - k0); ++k) {
-        const float w = __shfl_sync(0xffffffffu, wk, k);
-        const float4 *v = reinterpret_cast<const float4 *>(part_of<PART>(plan, cta, k0 + k) + 2 * ROWS + r * D);
+    float4 o[CN] = {};
+    auto add = [&](const float4(&y)[CN], float w) {
 #pragma unroll
-        for (int c = 0; c < (COLS + 31) / 32; ++c) {
-          const float4 y = COLS >= 32 || lane < COLS ? v[c * 32 + lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          o[c].x = fmaf(w, y.x, o[c].x), o[c].y = fmaf(w, y.y, o[c].y);
-          o[c].z = fmaf(w, y.z, o[c].z), o[c].w = fmaf(w, y.w, o[c].w);
-        }
+      for (int c = 0; c < CN; ++c) {
+        o[c].x = fmaf(w, y[c].x, o[c].x), o[c].y = fmaf(w, y[c].y, o[c].y);
+        o[c].z = fmaf(w, y[c].z, o[c].z), o[c].w = fmaf(w, y[c].w, o[c].w);
+      }
+    };
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      if (k0 > 0) {
+        const float *p = part_of<PART>(plan, cta, min(k0 + lane, n - 1));
+        mk = p[r], lk = k0 + lane < n ? p[ROWS + r] : 0.0f;
+      }
+      const float wk = exp2_approx(mk - m);
+      l = fmaf(wk, lk, l);
+      if (k0 == 0) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+          if (k < n) add(early[k], __shfl_sync(0xffffffffu, wk, k));
+      }
+#pragma unroll 4
+      for (int k = k0 == 0 ? AHEAD : 0; k < min(32, n - k0); ++k) {
+        float4 y[CN];
+        columns(y, k0 + k);
+        add(y, __shfl_sync(0xffffffffu, wk, k));
       }
     }
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
 #pragma unroll
-    for (int c = 0; c < (COLS + 31) / 32; ++c)
+    for (int c = 0; c < CN; ++c)
       if (COLS >= 32 || lane < COLS) put_out<D>(a, seq, h, row0 + r, c * 32 + lane, o[c], m, l);
   }
 }
@@ -1027,7 +1048,7 @@ template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) join_many_kernel(const __grid_constant__ AttentionArgs a,
                                                         const __grid_constant__ Plan plan) {
   constexpr int PART = ROWS * (D + 2), COLS = D / 4, kThreads = kJoinThreads, kWarps = kThreads / 32;
-  constexpr int SHARES = kThreads / COLS, MOST = kMostCtas * kSms;
+  constexpr int SHARES = kThreads / COLS, MOST = kMostCtas * kSms, AHEAD = 6;
   __shared__ float weights[MOST], red[2][kWarps];
   __shared__ float4 sums[SHARES][COLS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = blockIdx.y, cta = blockIdx.x;
@@ -1041,6 +1062,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_many_kernel(const __grid_co
   const int n = x.last - cta + 1;
   auto part = [&](int k) { return part_of<PART>(plan, cta, k); };
   float m = -1e30f, l = 0.0f, mk[(MOST + kThreads - 1) / kThreads], lk[(MOST + kThreads - 1) / kThreads];
+  // (the columns of the first parts are asked for before it is known what they weigh)
+  const int c = tid % COLS, share = tid / COLS;
+  auto columns = [&](int k) { return reinterpret_cast<const float4 *>(part(k) + 2 * ROWS)[r * COLS + c]; };
+  float4 early[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (share + i * SHARES < n) early[i] = columns(share + i * SHARES);
 #pragma unroll
   for (int i = 0; i < (MOST + kThreads - 1) / kThreads; ++i) {
     const int k = tid + i * kThreads;
@@ -1065,14 +1093,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_many_kernel(const __grid_co
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if (lane == 0) red[1][warp] = l;
   __syncthreads();
-  const int c = tid % COLS, share = tid / COLS;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int k = share; k < n; k += SHARES) {
-    const float w = weights[k];
-    const float4 v = reinterpret_cast<const float4 *>(part(k) + 2 * ROWS)[r * COLS + c];
+  auto add = [&](const float4 &v, float w) {
     o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (share + i * SHARES < n) add(early[i], weights[share + i * SHARES]);
+#pragma unroll 4
+  for (int k = share + AHEAD * SHARES; k < n; k += SHARES) add(columns(k), weights[k]);
   sums[share][c] = o;
   __syncthreads();
   if (tid < COLS) {
