@@ -493,6 +493,7 @@ aq_status aq_nvfp4_matmul(const uint16_t *x_bf16, int64_t M, int64_t K, const ui
  *   16 rows of K codes (D*bits/8 bytes a row, packed LSB first),
  *   16 rows of V codes,
  *   16 rows of fp16 pairs (scale, bias): the row's D/G pairs of K, then of V.
+ * aq_kv_append writes no scale below 0; a cache that was filled otherwise may have some.
  * Sequence b's position p lies in page table[b][p / page_size], there in row
  * p % page_size.  lens[b] is the sequence's length, the rows that a call writes
  * included.  A position whose table entry lies outside [0, pages), or at or

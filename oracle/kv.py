@@ -107,9 +107,9 @@ def attention(c: Cache, q_bits, scale: float, window: int = 0):
     """q_bits: bf16 patterns [batch, tokens, q_heads, D] -> a dict of 64-bit arrays:
 
     out [.., D] and lse [..], the attention; and for bounds of rounding errors
-    spread [.., D] = sum_t w_t scale_t code_td, size [.., D] = sum_t w_t |v_td| (w: the softmax weights),
-    terms [..] = max_t |scale| sum_d |q_d| (scale_t code_td + |bias_t|), the size of what a score is summed from, and
-    least [..] = n max scale_t max code over V of the n positions that any of the sequence's tokens sees."""
+    spread [.., D] = sum_t w_t |scale_t| code_td, size [.., D] = sum_t w_t |v_td| (w: the softmax weights),
+    terms [..] = max_t |scale| sum_d |q_d| (|scale_t| code_td + |bias_t|), the size of what a score is summed from, and
+    least [..] = n max |scale_t| max code over V of the n positions that any of the sequence's tokens sees."""
     q = f32(q_bits).astype(np.float64)
     B, n, hq, D = q.shape
     out, spread, size = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
@@ -124,7 +124,7 @@ def attention(c: Cache, q_bits, scale: float, window: int = 0):
                 continue
             k, v = ([np.stack(x) for x in zip(*(_fields(c, b, p, h, which) for p in known))] for which in (0, 1))
             kx, vx = k[0] * k[1] + k[2], v[0] * v[1] + v[2]
-            least[b, :, h * rep:(h + 1) * rep] = len(known) * max(v[1].max(), 2.0**-15) * (2**c.bits - 1)
+            least[b, :, h * rep:(h + 1) * rep] = len(known) * max(np.abs(v[1]).max(), 2.0**-15) * (2**c.bits - 1)
             pos = np.array(known)
             for j in range(n):
                 p = length - n + j
@@ -138,9 +138,9 @@ def attention(c: Cache, q_bits, scale: float, window: int = 0):
                     lse[b, j, i] = m + np.log(w.sum())
                     w /= w.sum()
                     out[b, j, i] = w @ vx[see]
-                    spread[b, j, i] = w @ (v[0] * v[1])[see]
+                    spread[b, j, i] = w @ (v[0] * np.abs(v[1]))[see]
                     size[b, j, i] = w @ np.abs(vx[see])
-                    terms[b, j, i] = abs(scale) * ((k[0] * k[1] + np.abs(k[2]))[see] @ np.abs(q[b, j, i])).max()
+                    terms[b, j, i] = abs(scale) * ((k[0] * np.abs(k[1]) + np.abs(k[2]))[see] @ np.abs(q[b, j, i])).max()
     return dict(out=out, lse=lse, spread=spread, size=size, terms=terms, least=least)
 
 
@@ -154,7 +154,7 @@ def attention_bounds(r: dict, D: int):
     partial sums and accumulations that follow one another: 2^-12), and the result rounds to bf16 (2^-8).
 
     Where the rounded product is subnormal its error is absolute instead, half a unit, 2^-25.  It stands for
-    2^(x - m) s with m = M + e - 13, M at most the row's maximum and 2^e at most twice the largest scale s of V (or 2^-14),
+    2^(x - m) s with m = M + e - 13, M at most the row's maximum and 2^e at most twice the largest magnitude s of a V scale (or 2^-14),
     and the result is divided by the sum of 2^(x - m), which is at least 2^(13 - e).  So a token's code adds an error of at most
     2^-25 2^(e - 13) code = 2^-38 2^e code <= 2^-37 max(s, 2^-15) code, and n tokens at most 2^-37 least."""
     e = ((D + 16) * 2.0**-23 * r["terms"] + 2.0**-21)[..., None]

@@ -208,7 +208,7 @@ struct State {
   float m[NT][RL], l[NT][RL];    // reference (see run_chunk) and sum of weights, the latter of this lane's tokens
   float bias[NT][F::kNG][RL];    // sum of weights times V biases, of this lane's tokens
   float acc[NT][D / 16][4];      // sum of (weight * V scale) * code, times 2^-24
-  int e;                         // V scales so far are below 2^e
+  int e;                         // magnitudes of V scales so far are below 2^e
 };
 
 // The query rows of a unit, as this lane's share of them: loaded early, looked at by start_unit.
@@ -458,7 +458,7 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
       }
   }
   // --- the running reference m of a row.  A weight is 2^(x - m), m = (a maximum so far) + e - 13, where V scales so far are
-  // at most 2^e (1 - 2^-11).  m stands while no weight times scale can pass fp16's 65504 = 2^16 (1 - 2^-11): scores at most 3
+  // at most 2^e (1 - 2^-11) in magnitude.  m stands while no weight times scale can pass fp16's 65504 = 2^16 (1 - 2^-11): scores at most 3
   // (a factor of 8) above the maximum it was taken from, scales within 2^e.  So a look at this lane's own values is enough
   // but for the first chunks and the rare new extreme.  (weight * scale) is a normal fp16 down to 2^-27 of the largest, and
   // below that its error is at most half a subnormal's unit, a 2^-38th of it.
@@ -468,7 +468,7 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
-      for (int gi = 0; gi < NG; ++gi) top = __hmax2(top, *reinterpret_cast<const __half2 *>(&sv[i][half][gi]));
+      for (int gi = 0; gi < NG; ++gi) top = __hmax2(top, __habs2(*reinterpret_cast<const __half2 *>(&sv[i][half][gi])));
   const uint32_t top_bits = __half_as_ushort(__low2half(top));
   float mx[NT][RL];
   bool more = static_cast<int>(top_bits >> 10) - 14 > st.e;
