@@ -154,8 +154,8 @@ def attention_bounds(r: dict, D: int):
     partial sums and accumulations that follow one another: 2^-12), and the result rounds to bf16 (2^-8).
 
     Where the rounded product is subnormal its error is absolute instead, half a unit, 2^-25.  It stands for
-    2^(x - m) s with m = M + e - 13, M at most the row's maximum and 2^e at most twice the largest magnitude s of a V scale (or 2^-14),
-    and the result is divided by the sum of 2^(x - m), which is at least 2^(13 - e).  So a token's code adds an error of at most
+    2^(x - M + 13 - e) s, M at most the row's maximum and 2^e at most twice the largest magnitude s of a V scale (or 2^-14), and the
+    result is divided by the sum of 2^(x - M + 13 - e), which is at least 2^(13 - e).  So a token's code adds an error of at most
     2^-25 2^(e - 13) code = 2^-38 2^e code <= 2^-37 max(s, 2^-15) code, and n tokens at most 2^-37 least."""
     e = ((D + 16) * 2.0**-23 * r["terms"] + 2.0**-21)[..., None]
     off = (2.0**-11 + 2.0**-12) * r["spread"] + (2 * e + 2.0**-12) * r["size"] + 2.0**-37 * r["least"][..., None]

@@ -6,8 +6,9 @@ import numpy as np
 import pytest
 import torch
 
-from kv_cases import queries
-from kv_stored import stored
+from kv_cases import bf16_bits, queries
+from kv_stored import pairs, places, stored
+from oracle import kv as ref
 from test_kv_gpu import _attend
 
 pytestmark = pytest.mark.gpu
@@ -49,3 +50,54 @@ def test_scales_below_zero(D, G, bits, signs):
     c = stored([150, 33], fill=fill, heads=2, D=D, G=G, bits=bits, seed=D + G)
     _attend(c, queries(2, 1, 8, D, 5))
     _attend(c, queries(2, 3, 8, D, 6), window=40)
+
+
+@pytest.mark.parametrize("q_heads", (4, 8, 16))
+def test_scores_far_from_zero(q_heads):
+    """Scores of tens of thousands that differ by little, beside V scales just below a power of two.  A warp's second chunk
+    holds a score that is a factor of about 8 above its first chunk's, where a weight is the largest it may be; at such a
+    size an fp32 has steps of 2^-8 to 2^-7 to tell."""
+    D, G, bits, B, n = 128, 32, 4, 64, 1024
+
+    def fill(rng, shape):
+        s, b = np.zeros(shape), np.zeros(shape)
+        s[..., 1, :] = 1.0 - 2.0**-11
+        b[..., 0, 0] = -30000.0
+        return s, b
+
+    c = stored([n] * B, fill=fill, page_size=64, D=D, G=G, bits=bits, seed=9)
+    at, rng = pairs(c).swapaxes(0, 1)[0], np.random.default_rng(10)
+    for b in range(B):
+        where = places(c, b, n)
+        k = at[where][:, 0, :, 1].copy()  # biases of K: the first group is a score's bulk, the others what it differs by
+        for first in range(0, n, 64):
+            k[first + 5, 0] = k[first + 40, 0] = 32 * rng.integers(1024, 2047)
+            k[first + 40, 1] = 2.0 + 0.0078125 * rng.integers(6, 14)
+            k[first + 40, 2] = 0.00390625 * rng.integers(0, 3)
+        at[where[0], where[1], where[2], 0, :, 1] = k
+    # a row's score is the sum of its token's biases: q = 1 in all of a group's 32 places, and the factor 1 / 32
+    q = bf16_bits(np.ones((B, 1, q_heads, D)))
+    _attend(c, q, scale=1 / 32)
+
+
+@pytest.mark.parametrize("bits", (4, 8))
+@pytest.mark.parametrize("v_scale", (1.0 - 2.0**-11, 2.0**-14, 2.0**-20, 65504.0))
+@pytest.mark.parametrize("size", (2.0**12, 2.0**20, -(2.0**22), 2.0**30, -(2.0**50)))
+def test_scores_so_far_apart_that_one_token_counts(size, v_scale, bits):
+    """Each row's softmax is one token's, so the row is that token's v.  What is off is the rounding to bf16 and that of the
+    weighted scale to fp16: 2^-8 of the value and 2^-11 of scale * code."""
+    D, G, n = 64, 32, 300
+
+    def fill(rng, shape):
+        s, b = np.zeros(shape), np.zeros(shape)
+        s[..., 1, :] = v_scale
+        b[..., 1, :] = -v_scale
+        b[..., 0, 0] = 100.0 + 0.5 * rng.permutation(int(np.prod(shape[:-2]))).reshape(shape[:-2])
+        return s, b
+
+    c = stored([n, 77], fill=fill, D=D, G=G, bits=bits, seed=11)
+    q = bf16_bits(np.full((2, 1, 6, D), size))
+    out, _ = _attend(c, q)
+    r = ref.attention(c, q, D**-0.5)
+    far = 2.0**-8 * np.abs(r["out"]) + (1 + 2.0**-8) * (2.0**-11 + 2.0**-20) * r["spread"]
+    assert (np.abs(out.float().cpu().numpy() - r["out"].reshape(out.shape)) <= far.reshape(out.shape)).all()

@@ -205,9 +205,9 @@ struct State {
   float rs[NT][RL];              // a raw score times this is a score in powers of 2
   int pos[NT][RL];               // the row's position
   int hi_all, lo_all;            // [lo_all, hi_all): positions seen by every row
-  float m[NT][RL], l[NT][RL];    // reference (see run_chunk) and sum of weights, the latter of this lane's tokens
-  float bias[NT][F::kNG][RL];    // sum of weights times V biases, of this lane's tokens
-  float acc[NT][D / 16][4];      // sum of (weight * V scale) * code, times 2^-24
+  float m[NT][RL], l[NT][RL];    // reference (see run_chunk) and sum of weights times 2^(13 - e), the latter of this lane's tokens
+  float bias[NT][F::kNG][RL];    // sum of weights times V biases, as l
+  float acc[NT][D / 16][4];      // sum of (weight * V scale) * code, times 2^(13 - e) 2^-24
   int e;                         // magnitudes of V scales so far are below 2^e
 };
 
@@ -457,11 +457,14 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
         }
       }
   }
-  // --- the running reference m of a row.  A weight is 2^(x - m), m = (a maximum so far) + e - 13, where V scales so far are
-  // at most 2^e (1 - 2^-11) in magnitude.  m stands while no weight times scale can pass fp16's 65504 = 2^16 (1 - 2^-11): scores at most 3
-  // (a factor of 8) above the maximum it was taken from, scales within 2^e.  So a look at this lane's own values is enough
-  // but for the first chunks and the rare new extreme.  (weight * scale) is a normal fp16 down to 2^-27 of the largest, and
-  // below that its error is at most half a subnormal's unit, a 2^-38th of it.
+  // --- the running reference m of a row: a maximum so far of its scores.  A weight is 2^(x - m), and is held times 2^(13 - e),
+  // where V scales so far are at most 2^e (1 - 2^-11) in magnitude.  m stands while no weight times scale can pass fp16's
+  // 65504 = 2^16 (1 - 2^-11): x - m at most 3 (a factor of 8), scales within 2^e.  So a look at this lane's own values is
+  // enough but for the first chunks and the rare new extreme.  What is compared with 3 is the difference that the weight is
+  // formed from, rounded score less reference: however large scores are, it is exact where it is small, and 0 for the
+  // largest.  (The product of raw score and factor less m, in one step, would be off by m's own rounding, and so would m with
+  // 13 - e in it.)  (weight * scale) is a normal fp16 down to 2^-27 of the largest, and below that its error is at most half a
+  // subnormal's unit, a 2^-38th of it.
   __half2 top = __half2half2(__ushort_as_half(0));  // (scale, bias): the low half is what counts; a NaN is passed over
 #pragma unroll
   for (int i = 0; i < CT; ++i)
@@ -476,11 +479,16 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < RL; ++c) {
+#pragma unroll
+      for (int i = 0; i < CT; ++i) {  // (the product is never contracted with the difference that follows)
+        const float2 y = __fmul2_rn(make_float2(x[i][nt][0][c], x[i][nt][1][c]), make_float2(st.rs[nt][c], st.rs[nt][c]));
+        x[i][nt][0][c] = y.x, x[i][nt][1][c] = y.y;
+      }
       float v = fmaxf(x[0][nt][0][c], x[0][nt][1][c]);
 #pragma unroll
       for (int i = 1; i < CT; ++i) v = fmaxf(v, fmaxf(x[i][nt][0][c], x[i][nt][1][c]));
       mx[nt][c] = v;
-      more |= fmaf(v, st.rs[nt][c], static_cast<float>(st.e - 16)) > st.m[nt][c];
+      more |= v - st.m[nt][c] > 3.0f;
     }
   if (__any_sync(0xffffffffu, more)) {
     const int e = max(st.e, static_cast<int>(__reduce_max_sync(0xffffffffu, top_bits) >> 10) - 14);
@@ -495,8 +503,8 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        const float mn = fmaxf(st.m[nt][c] + shift, fmaf(v, st.rs[nt][c], static_cast<float>(e - 13)));
-        al[c] = exp2_approx(st.m[nt][c] - mn);
+        const float mn = fmaxf(st.m[nt][c], v);
+        al[c] = exp2_approx(st.m[nt][c] - mn - shift);
         st.m[nt][c] = mn;
         st.l[nt][c] *= al[c];
 #pragma unroll
@@ -509,14 +517,17 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
     }
   }
   // --- weights, and their products with V
+  const float room = static_cast<float>(13 - st.e);
 #pragma unroll
   for (int i = 0; i < CT; ++i) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < RL; ++c) {
-        x[i][nt][0][c] = exp2_approx(fmaf(x[i][nt][0][c], st.rs[nt][c], -st.m[nt][c]));
-        x[i][nt][1][c] = exp2_approx(fmaf(x[i][nt][1][c], st.rs[nt][c], -st.m[nt][c]));
+        const float2 y = fadd2(make_float2(x[i][nt][0][c], x[i][nt][1][c]), make_float2(-st.m[nt][c], -st.m[nt][c]));
+        const float2 z = fadd2(y, make_float2(room, room));
+        x[i][nt][0][c] = exp2_approx(z.x);
+        x[i][nt][1][c] = exp2_approx(z.y);
         st.l[nt][c] += x[i][nt][0][c] + x[i][nt][1][c];
       }
     const uint8_t *v = stage + i * F::kTileBytes + kTile * F::kRow + t * F::kRow + g * (F::kGroupBytes / 8);
@@ -579,11 +590,12 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
   }
 }
 
-// Sums over the lanes that share rows, then the accumulator in its true size: acc[nt][k][half * 2 + col(gi, c)] becomes the
+// Sums over the lanes that share rows, then all sums in their true size: acc[nt][k][half * 2 + col(gi, c)] becomes the
 // weighted sum of dimension gi * G + g * (G / 8) + 2 (k % (G / 16)) + half, gi = k / (G / 16), for row row_of(nt, t, c).
 template <int BITS, int D, int G, int ROWS>
 AQ_DEVICE void finish_unit(State<BITS, D, G, ROWS> &st) {
   using F = Form<BITS, D, G, ROWS>;
+  const float one = __uint_as_float(static_cast<uint32_t>(127 - 13 + st.e) << 23), even = one * 0x1p24f, odd = BITS == 4 ? one * 0x1p20f : even;
 #pragma unroll
   for (int nt = 0; nt < F::kNT; ++nt)
 #pragma unroll
@@ -594,12 +606,13 @@ AQ_DEVICE void finish_unit(State<BITS, D, G, ROWS> &st) {
 #pragma unroll
         for (int gi = 0; gi < F::kNG; ++gi) st.bias[nt][gi][c] += __shfl_xor_sync(0xffffffffu, st.bias[nt][gi][c], o);
       }
+      st.l[nt][c] *= one;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const int gi = k / (G / 16), col = F::col(gi, c);
-        const float b = st.bias[nt][gi][c];
-        st.acc[nt][k][col] = fmaf(st.acc[nt][k][col], 0x1p24f, b);
-        st.acc[nt][k][2 + col] = fmaf(st.acc[nt][k][2 + col], BITS == 4 ? 0x1p20f : 0x1p24f, b);
+        const float b = st.bias[nt][gi][c] * one;
+        st.acc[nt][k][col] = fmaf(st.acc[nt][k][col], even, b);
+        st.acc[nt][k][2 + col] = fmaf(st.acc[nt][k][2 + col], odd, b);
       }
     }
 }
