@@ -101,3 +101,27 @@ def test_scores_so_far_apart_that_one_token_counts(size, v_scale, bits):
     r = ref.attention(c, q, D**-0.5)
     far = 2.0**-8 * np.abs(r["out"]) + (1 + 2.0**-8) * (2.0**-11 + 2.0**-20) * r["spread"]
     assert (np.abs(out.float().cpu().numpy() - r["out"].reshape(out.shape)) <= far.reshape(out.shape)).all()
+
+
+@pytest.mark.parametrize("lens,width", [([1], None), ([300, 40, 0], None), ([700, 3, 40], 512)])
+@pytest.mark.parametrize("size", (2.0**80, 2.0**95))
+def test_scores_far_below_zero(size, lens, width):
+    """Every score of a row is below -2^80: the row still is the softmax of what it sees.  k = 100 to 250, q = -size."""
+    D, G, bits = 64, 32, 4
+
+    def fill(rng, shape):
+        s, b = np.zeros(shape), np.zeros(shape)
+        s[..., 1, :] = 0.25
+        return s, b
+
+    c = stored(lens, fill=fill, D=D, G=G, bits=bits, seed=13, width=width)
+    at, rng = pairs(c).swapaxes(0, 1)[0], np.random.default_rng(14)
+    for b, n in enumerate(lens):
+        page, tile, row = places(c, b, n)
+        at[page, tile, row, 0, 0, 1] = 100.0 + 0.125 * rng.permutation(1200)[:n]
+    q = bf16_bits(np.full((len(lens), 2, 4, D), -size))
+    out, lse = _attend(c, q)
+    r = ref.attention(c, q, D**-0.5)
+    far = 2.0**-8 * np.abs(r["out"]) + (1 + 2.0**-8) * (2.0**-11 + 2.0**-20) * r["spread"]
+    assert (np.abs(out.float().cpu().numpy() - r["out"]) <= far).all()
+    assert torch.isneginf(lse).cpu().numpy().sum() == np.isneginf(r["lse"]).sum()

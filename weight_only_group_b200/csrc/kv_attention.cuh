@@ -30,6 +30,7 @@
 // always in the order of the tokens, so results repeat bit for bit.
 #pragma once
 
+#include <cfloat>
 #include <math_constants.h>
 
 #include <algorithm>
@@ -47,6 +48,7 @@ __device__ uint32_t g_fault = 0;
 constexpr int kSms = 148;         // the grid never has more CTAs than these hold
 constexpr int kMostCtas = 3;      // of an SM
 constexpr int kJoinThreads = 256;
+constexpr float kLowest = -FLT_MAX;  // the reference of a row that has seen nothing: below any score, and finite
 // Where units are no more than the GPU holds CTAs, and none can have more than this many bytes of cache for each warp of a
 // CTA (twice as many where there are enough units for nearly every SM), a CTA takes a unit: no list of places, no second
 // kernel.  Measured against the list (4 bits, D = 128, four rows, 8 warps: 4 chunks of 32 tokens a warp are 1024 tokens): 8
@@ -329,7 +331,7 @@ AQ_DEVICE void start_unit(State<BITS, D, G, ROWS> &st, const Queries<BITS, D, G,
     for (int c = 0; c < RL; ++c) {
       st.rs[nt][c] = __shfl_sync(0xffffffffu, rs, (2 * t + c) * 4);
       st.pos[nt][c] = position(row0 + F::row_of(nt, t, c));
-      st.m[nt][c] = -1e30f;
+      st.m[nt][c] = kLowest;
       st.l[nt][c] = 0.0f;
 #pragma unroll
       for (int gi = 0; gi < F::kNG; ++gi) st.bias[nt][gi][c] = 0.0f;
@@ -698,7 +700,7 @@ AQ_DEVICE void join_rows(int n, int r0, Part part, Put put) {
   const float *p = part(min(mine, n - 1));
 #pragma unroll
   for (int i = 0; i < RN; ++i) {
-    m[i] = wk[i] = mine < n ? p[r0 + i * STEP] : -1e30f;
+    m[i] = wk[i] = mine < n ? p[r0 + i * STEP] : kLowest;
     l[i] = mine < n ? p[ROWS + r0 + i * STEP] : 0.0f;
   }
 #pragma unroll
@@ -1006,7 +1008,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_few_kernel(const __grid_con
   for (int r = warp; r < ROWS && row0 + r < a.tokens * a.group; r += kJoinThreads / 32) {
     // a lane looks after the reference and the weights' sum of a part, 32 parts at a time; the columns of the first parts are
     // asked for before it is known what they weigh
-    float mk = lane < n ? part_of<PART>(plan, cta, lane)[r] : -1e30f, lk = lane < n ? part_of<PART>(plan, cta, lane)[ROWS + r] : 0.0f;
+    float mk = lane < n ? part_of<PART>(plan, cta, lane)[r] : kLowest, lk = lane < n ? part_of<PART>(plan, cta, lane)[ROWS + r] : 0.0f;
     auto columns = [&](float4(&y)[CN], int k) {
       const float4 *v = reinterpret_cast<const float4 *>(part_of<PART>(plan, cta, k) + 2 * ROWS + r * D);
 #pragma unroll
@@ -1074,7 +1076,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_many_kernel(const __grid_co
   if (row >= a.tokens * a.group) return;
   const int n = x.last - cta + 1;
   auto part = [&](int k) { return part_of<PART>(plan, cta, k); };
-  float m = -1e30f, l = 0.0f, mk[(MOST + kThreads - 1) / kThreads], lk[(MOST + kThreads - 1) / kThreads];
+  float m = kLowest, l = 0.0f, mk[(MOST + kThreads - 1) / kThreads], lk[(MOST + kThreads - 1) / kThreads];
   // (the columns of the first parts are asked for before it is known what they weigh)
   const int c = tid % COLS, share = tid / COLS;
   auto columns = [&](int k) { return reinterpret_cast<const float4 *>(part(k) + 2 * ROWS)[r * COLS + c]; };
@@ -1085,7 +1087,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_many_kernel(const __grid_co
 #pragma unroll
   for (int i = 0; i < (MOST + kThreads - 1) / kThreads; ++i) {
     const int k = tid + i * kThreads;
-    mk[i] = k < n ? part(k)[r] : -1e30f;
+    mk[i] = k < n ? part(k)[r] : kLowest;
     lk[i] = k < n ? part(k)[ROWS + r] : 0.0f;
     m = fmaxf(m, mk[i]);
   }
