@@ -125,3 +125,10 @@ def test_scores_far_below_zero(size, lens, width):
     far = 2.0**-8 * np.abs(r["out"]) + (1 + 2.0**-8) * (2.0**-11 + 2.0**-20) * r["spread"]
     assert (np.abs(out.float().cpu().numpy() - r["out"]) <= far).all()
     assert torch.isneginf(lse).cpu().numpy().sum() == np.isneginf(r["lse"]).sum()
+
+
+def test_a_factor_near_the_largest_number():
+    """Queries of 2^-128 under a factor near fp32's largest: scores of a usual size."""
+    c = stored([60, 9], fill=lambda rng, shape: (rng.uniform(0.01, 0.1, shape), rng.uniform(-2, 0, shape)), D=64, G=32, bits=4, seed=15)
+    q = np.random.default_rng(16).standard_normal((2, 1, 4, 64)) * 2.0**-128
+    _attend(c, bf16_bits(q), scale=3e38)

@@ -326,7 +326,7 @@ AQ_DEVICE void start_unit(State<BITS, D, G, ROWS> &st, const Queries<BITS, D, G,
       }
     }
     // (a scale of 0 as the smallest there is, so that what is not seen keeps its -infinity)
-    const float rs = fmaxf(ldexpf(fabsf(a.scale) * CUDART_L2E_F, 24 - e), 0x1p-126f);
+    const float rs = fmaxf(ldexpf(fabsf(a.scale), 24 - e) * CUDART_L2E_F, 0x1p-126f);
 #pragma unroll
     for (int c = 0; c < RL; ++c) {
       st.rs[nt][c] = __shfl_sync(0xffffffffu, rs, (2 * t + c) * 4);
