@@ -132,3 +132,32 @@ def test_a_factor_near_the_largest_number():
     c = stored([60, 9], fill=lambda rng, shape: (rng.uniform(0.01, 0.1, shape), rng.uniform(-2, 0, shape)), D=64, G=32, bits=4, seed=15)
     q = np.random.default_rng(16).standard_normal((2, 1, 4, 64)) * 2.0**-128
     _attend(c, bf16_bits(q), scale=3e38)
+
+
+@pytest.mark.parametrize("bits", (4, 8))
+def test_queries_with_elements_of_very_different_sizes(bits):
+    """Elements down to 2^-28 of their row's largest count in full: the largest meets keys of 0, and the factor makes the
+    rest a score of some size."""
+    D, G, B = 64, 32, 3
+
+    def fill(rng, shape):
+        s, b = np.zeros(shape), np.zeros(shape)
+        s[..., 0, 1] = rng.uniform(10, 60, shape[:-2]) * 2.0 ** (8 - bits)
+        s[..., 1, :] = 0.1
+        return s, b
+
+    c = stored([50, 7, 90], fill=fill, D=D, G=G, bits=bits, seed=17)
+    rng = np.random.default_rng(18)
+    q = np.zeros((B, 1, 4, D))
+    q[..., 3] = 1.0
+    q[..., 32:] = rng.choice((-1, 1), (B, 1, 4, 32)) * 2.0**-28 * (1 + rng.integers(64, 128, (B, 1, 4, 32)) / 128)
+    _attend(c, bf16_bits(q), scale=2.0**14)
+
+
+def test_queries_below_the_normal_numbers():
+    """Rows of the smallest bf16 there are, and a factor that makes scores of them."""
+    D, G, bits = 64, 32, 8
+    c = stored([60, 9], fill=lambda rng, shape: (rng.uniform(0.01, 0.1, shape), rng.uniform(-9, 0, shape)), D=D, G=G, bits=bits, seed=19)
+    rng = np.random.default_rng(20)
+    q = rng.integers(-255, 256, (2, 1, 4, D)) * 2.0 ** -np.array([133.0, 130.0, 120.0, 110.0])[:, None]
+    _attend(c, bf16_bits(q), scale=2.0**110)

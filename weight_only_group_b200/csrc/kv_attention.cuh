@@ -287,8 +287,10 @@ AQ_DEVICE void start_unit(State<BITS, D, G, ROWS> &st, const Queries<BITS, D, G,
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     if (F::kPair) top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
-    // 2^e puts the row's largest |q| in [2^14, 2^15): bf16's 8 bits are exact in fp16 down to 2^-28 of it
-    const int e = min(120, max(-100, 141 - static_cast<int>(top >> 7)));
+    // 2^e puts the row's largest |q| in [2^15, 2^16), where bf16 ends at 65280: its 8 bits are exact in fp16, whose last place is
+    // 2^-24, down to 2^-28 of the largest where they also go in as a 16th (4 bits), to 2^-32 where not.  Rows below 2^-105, for
+    // which e would be too large, are exact as they are: a bf16 has no place below 2^-133.
+    const int e = min(120, max(-100, 142 - static_cast<int>(top >> 7)));
     const float up = __uint_as_float((static_cast<uint32_t>(e + 127) << 23) | (__float_as_uint(a.scale) & 0x80000000u));
     const float up4 = BITS == 4 ? up * 0.0625f : up;
     float sum[4];
