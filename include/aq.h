@@ -560,8 +560,11 @@ aq_status aq_kv_read(const aq_kv_cache *cache, int64_t rows, const int32_t *offs
  * Arithmetic: scores from the exact codes and q as fp16 under a power-of-two
  * factor of its row (exact for elements down to 2^-28 of the row's largest);
  * softmax weights and all sums in fp32; the product of a weight and a V scale
- * rounds to fp16 (11 bits; below a 2^-27th of the row's largest product fewer,
- * down to an error of a 2^-38th of it).  q must be finite, q and scale*q below
+ * rounds to fp16, which is relative to code*scale, not to the value that the bias
+ * makes of it: 11 bits, and fewer below a 2^-27th of P, down to an error of a
+ * 2^-38th of P, which is the row's largest weight times the largest magnitude of a
+ * V scale of any token and group that any of the sequence's new tokens sees (or
+ * 2^-14, where that is larger), rounded up to a power of two.  q must be finite, q and scale*q below
  * 2^100 and scores below 2^126 in magnitude.
  * workspace: aq_kv_attention_workspace_bytes bytes, 16-byte aligned, for partial
  * results; it needs no preparation and must not be used by another call in flight.

@@ -467,8 +467,9 @@ AQ_DEVICE void run_chunk(State<BITS, D, G, ROWS> &st, const AttentionArgs &a, co
   // enough but for the first chunks and the rare new extreme.  What is compared with 3 is the difference that the weight is
   // formed from, rounded score less reference: however large scores are, it is exact where it is small, and 0 for the
   // largest.  (The product of raw score and factor less m, in one step, would be off by m's own rounding, and so would m with
-  // 13 - e in it.)  (weight * scale) is a normal fp16 down to 2^-27 of the largest, and below that its error is at most half a
-  // subnormal's unit, a 2^-38th of it.
+  // 13 - e in it.)  With the row's largest weight as 2^(13 - e), (weight * scale) is a normal fp16 down to a 2^-27th of that weight
+  // times 2^e, and below that its error is at most half a subnormal's unit, a 2^-38th of it.  e is one for all rows and groups of
+  // the unit.
   __half2 top = __half2half2(__ushort_as_half(0));  // (scale, bias): the low half is what counts; a NaN is passed over
 #pragma unroll
   for (int i = 0; i < CT; ++i)
