@@ -100,13 +100,13 @@ struct Form {
   static constexpr int kThreads = kWarps * 32;
   static_assert(kRing >= kPart * 4, "a warp's ring holds its last partial result");
   static_assert(kCtas * (kWarps * kRing + 4 * 1024) <= 228 * 1024, "the CTAs of an SM share its memory");
-  static_assert(kCtas <= kMostCtas, "the join kernels' room for parts");
+  static_assert(kCtas <= kMostCtas, "the join kernel's room for parts");
 };
 
-// What a CTA leaves for the join: the unit that starts in its run and goes on
-// behind it (or -1), and the last CTA that has a part of it.
+// What a CTA leaves for the join: the unit that goes on behind its run (or -1),
+// and the first and the last CTA that have a part of it.
 struct Loose {
-  int unit, last;
+  int unit, first, last;
 };
 
 struct Plan {
@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D
   extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings
   __shared__ uint64_t bars[kWarps][F::kStages];
   __shared__ int sums[kThreads + 1], warp_sums[kWarps];
-  __shared__ int head_unit[kWarps], tail_unit[kWarps], tail_end[kWarps];
+  __shared__ int head_unit[kWarps], tail_unit[kWarps], tail_first[kWarps], tail_end[kWarps];
   __shared__ bool tail_starts[kWarps];
   __shared__ volatile int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -927,7 +927,8 @@ __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D
             head_unit[warp] = id;
           } else {
             tail_unit[warp] = id;
-            tail_end[warp] = at - first - take + cur.span.chunks;  // the place behind the unit
+            tail_first[warp] = at - first - take;                   // the place of the unit's first chunk
+            tail_end[warp] = tail_first[warp] + cur.span.chunks;    // the place behind the unit
             tail_starts[warp] = first == 0;
           }
         }
@@ -948,7 +949,7 @@ __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D
   __syncthreads();
   // --- what units have left at the warps' ends, in their order: the end of one that an earlier warp began (head), and the
   // beginning or the middle of one that the next warp goes on with (tail)
-  Loose loose{-1, -1};
+  Loose loose{-1, -1, -1};
   if (!abort_flag) {
     // slot 2 w: warp w's head, slot 2 w + 1: its tail; lane s looks at slot s
     static_assert(2 * kWarps <= 32, "a lane for each slot");
@@ -963,7 +964,7 @@ __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D
       const uint32_t members = used & ((firsts & -firsts) - 1u) & ~((1u << first) - 1u);  // (0 - 1: all the rest)
       const int n = __popc(members), last = 31 - __clz(members), id = __shfl_sync(0xffffffffu, mine, first);
       const bool starts = (first & 1) && tail_starts[first >> 1], ends = !(last & 1);
-      if (starts && !ends) loose = Loose{id, (tail_end[first >> 1] - 1) / (kWarps * share)};
+      if (!ends) loose = Loose{id, tail_first[first >> 1] / (kWarps * share), (tail_end[first >> 1] - 1) / (kWarps * share)};
       const float *end_part = plan.heads + (int64_t(blockIdx.x) * kWarps + (last >> 1)) * F::kPart;
       auto part = [&](int k) -> const float * {
         return ends && k == n - 1 ? end_part : reinterpret_cast<const float *>(smem + ((first >> 1) + k) * F::kRing);
@@ -988,96 +989,72 @@ __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D
   if (threadIdx.x == 0 && !plan.direct) plan.loose[blockIdx.x] = loose;
 }
 
-// The join kernels: they join the units that several CTAs have a part of.  The first part of a unit is what CTA `cta` has at
-// its end, the others what the CTAs behind it have at their beginnings.
+// The join kernel: it joins the units that several CTAs have a part of.  The first part of a unit is what CTA `cta`, its first,
+// has at its end, the others what the CTAs behind it have at their beginnings.  How many parts a unit has goes by the
+// sequences' lengths, which the host does not know, so the blocks look: up to kFew of them are joined by the block of the first
+// CTA, a warp for each row; of a unit with more, block first + r takes row r with all its threads.  Measured (4 bits, D = 128,
+// four rows, one KV head, 64 sequences, one of them of 65536 tokens and 296 parts): 47.2 us with all of a row's parts read by one warp,
+// 14.2 us this way.
 template <int PART>
 AQ_DEVICE const float *part_of(const Plan &plan, int cta, int k) {
   return plan.parts + (int64_t(cta + k) * 2 + (k == 0 ? 1 : 0)) * PART;
 }
 
-// Where units are many, and have few parts each: block i takes the one that starts in CTA i's run and goes on behind it, and a
-// warp a row of it.
+// Row r of a unit of n parts, by a warp: it has the parts of a row on their way at once or twice.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) join_few_kernel(const __grid_constant__ AttentionArgs a,
-                                                                const __grid_constant__ Plan plan) {
+AQ_DEVICE void join_by_warp(const AttentionArgs &a, const Plan &plan, int cta, int n, int r, int seq, int h, int row) {
   constexpr int PART = ROWS * (D + 2), COLS = D / 4, CN = (COLS + 31) / 32, AHEAD = 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
-  await_previous();
-  const Loose x = plan.loose[cta];
-  if (x.unit < 0) return;
-  const int units = a.c.heads * plan.row_tiles;
-  const int seq = x.unit / units, u = x.unit - seq * units, h = u / plan.row_tiles, row0 = (u - h * plan.row_tiles) * ROWS;
-  const int n = x.last - cta + 1;
-  for (int r = warp; r < ROWS && row0 + r < a.tokens * a.group; r += kJoinThreads / 32) {
-    // a lane looks after the reference and the weights' sum of a part, 32 parts at a time; the columns of the first parts are
-    // asked for before it is known what they weigh
-    float mk = lane < n ? part_of<PART>(plan, cta, lane)[r] : kLowest, lk = lane < n ? part_of<PART>(plan, cta, lane)[ROWS + r] : 0.0f;
-    auto columns = [&](float4(&y)[CN], int k) {
-      const float4 *v = reinterpret_cast<const float4 *>(part_of<PART>(plan, cta, k) + 2 * ROWS + r * D);
+  const int lane = threadIdx.x & 31;
+  // a lane looks after the reference and the weights' sum of a part; the columns of the first parts are asked for before it is
+  // known what they weigh
+  const float mk = lane < n ? part_of<PART>(plan, cta, lane)[r] : kLowest;
+  const float lk = lane < n ? part_of<PART>(plan, cta, lane)[ROWS + r] : 0.0f;
+  auto columns = [&](float4(&y)[CN], int k) {
+    const float4 *v = reinterpret_cast<const float4 *>(part_of<PART>(plan, cta, k) + 2 * ROWS + r * D);
 #pragma unroll
-      for (int c = 0; c < CN; ++c) y[c] = COLS >= 32 || lane < COLS ? v[c * 32 + lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    };
-    float4 early[AHEAD][CN];
+    for (int c = 0; c < CN; ++c) y[c] = COLS >= 32 || lane < COLS ? v[c * 32 + lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
+  float4 early[AHEAD][CN];
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k)
-      if (k < n) columns(early[k], k);
-    float m = mk, l = 0.0f;
-    for (int k = lane + 32; k < n; k += 32) m = fmaxf(m, part_of<PART>(plan, cta, k)[r]);
+  for (int k = 0; k < AHEAD; ++k)
+    if (k < n) columns(early[k], k);
+  float m = mk;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float4 o[CN] = {};
-    auto add = [&](const float4(&y)[CN], float w) {
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float4 o[CN] = {};
+  auto add = [&](const float4(&y)[CN], float w) {
 #pragma unroll
-      for (int c = 0; c < CN; ++c) {
-        o[c].x = fmaf(w, y[c].x, o[c].x), o[c].y = fmaf(w, y[c].y, o[c].y);
-        o[c].z = fmaf(w, y[c].z, o[c].z), o[c].w = fmaf(w, y[c].w, o[c].w);
-      }
-    };
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      if (k0 > 0) {
-        const float *p = part_of<PART>(plan, cta, min(k0 + lane, n - 1));
-        mk = p[r], lk = k0 + lane < n ? p[ROWS + r] : 0.0f;
-      }
-      const float wk = exp2_approx(mk - m);
-      l = fmaf(wk, lk, l);
-      if (k0 == 0) {
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-          if (k < n) add(early[k], __shfl_sync(0xffffffffu, wk, k));
-      }
-#pragma unroll 4
-      for (int k = k0 == 0 ? AHEAD : 0; k < min(32, n - k0); ++k) {
-        float4 y[CN];
-        columns(y, k0 + k);
-        add(y, __shfl_sync(0xffffffffu, wk, k));
-      }
+    for (int c = 0; c < CN; ++c) {
+      o[c].x = fmaf(w, y[c].x, o[c].x), o[c].y = fmaf(w, y[c].y, o[c].y);
+      o[c].z = fmaf(w, y[c].z, o[c].z), o[c].w = fmaf(w, y[c].w, o[c].w);
     }
+  };
+  const float wk = exp2_approx(mk - m);
+  float l = wk * lk;
 #pragma unroll
-    for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
-#pragma unroll
-    for (int c = 0; c < CN; ++c)
-      if (COLS >= 32 || lane < COLS) put_out<D>(a, seq, h, row0 + r, c * 32 + lane, o[c], m, l);
+  for (int k = 0; k < AHEAD; ++k)
+    if (k < n) add(early[k], __shfl_sync(0xffffffffu, wk, k));
+#pragma unroll 4
+  for (int k = AHEAD; k < n; ++k) {
+    float4 y[CN];
+    columns(y, k);
+    add(y, __shfl_sync(0xffffffffu, wk, k));
   }
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+#pragma unroll
+  for (int c = 0; c < CN; ++c)
+    if (COLS >= 32 || lane < COLS) put_out<D>(a, seq, h, row, c * 32 + lane, o[c], m, l);
 }
 
-// Where units are few and have many parts: block (i, r) takes row r of it, and its threads share the parts (up to as many
-// as there are CTAs) as well as the columns.
+// Row r of a unit of n parts, by a block: its threads share the parts (up to as many as there are CTAs) as well as the columns.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) join_many_kernel(const __grid_constant__ AttentionArgs a,
-                                                        const __grid_constant__ Plan plan) {
+AQ_DEVICE void join_by_block(const AttentionArgs &a, const Plan &plan, int cta, int n, int r, int seq, int h, int row) {
   constexpr int PART = ROWS * (D + 2), COLS = D / 4, kThreads = kJoinThreads, kWarps = kThreads / 32;
   constexpr int SHARES = kThreads / COLS, MOST = kMostCtas * kSms, AHEAD = 6;
   __shared__ float weights[MOST], red[2][kWarps];
   __shared__ float4 sums[SHARES][COLS];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = blockIdx.y, cta = blockIdx.x;
-  await_previous();
-  const Loose x = plan.loose[cta];
-  if (x.unit < 0) return;
-  const int units = a.c.heads * plan.row_tiles;
-  const int seq = x.unit / units, u = x.unit - seq * units, h = u / plan.row_tiles;
-  const int row = (u - h * plan.row_tiles) * ROWS + r;
-  if (row >= a.tokens * a.group) return;
-  const int n = x.last - cta + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto part = [&](int k) { return part_of<PART>(plan, cta, k); };
   float m = kLowest, l = 0.0f, mk[(MOST + kThreads - 1) / kThreads], lk[(MOST + kThreads - 1) / kThreads];
   // (the columns of the first parts are asked for before it is known what they weigh)
@@ -1136,6 +1113,26 @@ __global__ void __launch_bounds__(kJoinThreads) join_many_kernel(const __grid_co
   }
 }
 
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttentionArgs a,
+                                                            const __grid_constant__ Plan plan) {
+  constexpr int kFew = ROWS > 8 ? ROWS : 8;  // (a unit of more parts goes on behind the runs of at least as many CTAs)
+  static_assert(kFew >= ROWS && kFew <= 32, "a block for each row; a lane for each part");
+  await_previous();
+  const Loose x = plan.loose[blockIdx.x];
+  if (x.unit < 0) return;
+  const int units = a.c.heads * plan.row_tiles, rows = a.tokens * a.group;
+  const int seq = x.unit / units, u = x.unit - seq * units, h = u / plan.row_tiles, row0 = (u - h * plan.row_tiles) * ROWS;
+  const int n = x.last - x.first + 1, behind = static_cast<int>(blockIdx.x) - x.first;
+  if (n > kFew) {
+    if (behind < ROWS && row0 + behind < rows)
+      join_by_block<D, ROWS>(a, plan, x.first, n, behind, seq, h, row0 + behind);
+  } else if (behind == 0) {
+    for (int r = threadIdx.x >> 5; r < ROWS && row0 + r < rows; r += kJoinThreads / 32)
+      join_by_warp<D, ROWS>(a, plan, x.first, n, r, seq, h, row0 + r);
+  }
+}
+
 struct Sizes {
   int ctas, row_tiles;
   bool direct;
@@ -1188,10 +1185,7 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream) {
   plan.loose = reinterpret_cast<Loose *>(ws + s.loose);
   e = launch_dependent(kern, dim3(s.ctas), F::kThreads, kBytes, stream, a, plan);
   if (e != cudaSuccess || s.direct || s.ctas == 1) return e;
-  // (up to eight parts a unit on average: a warp has those of a row on their way at once or twice)
-  if (int64_t(s.ctas) <= 8 * int64_t(a.c.batch) * a.c.heads * s.row_tiles)
-    return launch_dependent(join_few_kernel<D, ROWS>, dim3(s.ctas), kJoinThreads, 0, stream, a, plan);
-  return launch_dependent(join_many_kernel<D, ROWS>, dim3(s.ctas, ROWS), kJoinThreads, 0, stream, a, plan);
+  return launch_dependent(join_kernel<D, ROWS>, dim3(s.ctas), kJoinThreads, 0, stream, a, plan);
 }
 
 // Calls run for a form: as many rows as a KV head has, up to 16; 8 where the accumulators of 16 rows do not fit a thread's
