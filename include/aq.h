@@ -577,13 +577,13 @@ aq_status aq_kv_attention(const aq_kv_cache *cache, const uint16_t *q_bf16, int6
 
 /* Bits of the device fault word. */
 enum {
-  AQ_FAULT_WAIT_MASK = 0x1Fu, /* bits 0-4: a kernel gave up a bounded wait and returned early */
+  AQ_FAULT_WAIT_MASK = 0x5Fu, /* bits 0-4, 6: a kernel gave up a bounded wait and returned early (6: aq_kv_attention) */
   AQ_FAULT_BAD_INDEX = 0x20u  /* an embedding id, an expert id or a page of a cache's table was out of range */
 };
 
 /* Limit, in SM clock cycles, of every bounded wait of the decode kernel (the
  * tensor-core QMV behind aq_matmul for M <= 8, the gather matmul and the
- * block-scaled decode matmuls) in launches made after this call, from any
+ * block-scaled decode matmuls) and of aq_kv_attention in launches made after this call, from any
  * thread; cycles <= 0 restores the default of 2e9 cycles (about one second).
  * No counterpart on the pages: it exists to test the timeout path.  A wait that
  * runs out sets a bit of AQ_FAULT_WAIT_MASK in the device fault word, the
@@ -592,8 +592,8 @@ enum {
  * HBM takes (a few thousand cycles) makes the waits run out on purpose. */
 void aq_set_wait_limit(int64_t cycles);
 
-/* on != 0: every decode-kernel launch made afterwards (from any thread) also
- * waits, after staging its activations, on a barrier that nothing completes,
+/* on != 0: every launch of the decode kernel and of aq_kv_attention made
+ * afterwards (from any thread) also waits, after staging its activations, on a barrier that nothing completes,
  * so that this bounded wait runs out (after aq_set_wait_limit's limit): the
  * launch sets its fault bit, issues no more work, waits for its own copies in
  * flight and returns, its output invalid.  on = 0 restores normal launches.
@@ -602,7 +602,7 @@ void aq_set_wait_stall(int on);
 
 /* Reads and clears the device-side fault word of the current device: non-zero
  * when a kernel gave up a bounded wait (an mbarrier that never completed) and
- * returned early, its output then invalid (bits 0-4), or when an embedding id,
+ * returned early, its output then invalid (bits 0-4, 6), or when an embedding id,
  * an expert id or a page of a cache's table was out of range (bit 5).
  * Synchronizes the device. */
 aq_status aq_device_fault(uint32_t *fault_word);

@@ -43,6 +43,7 @@ AQ_KERNEL_QMM = 2
 AQ_KERNEL_QMV_TCGEN05 = 3
 AQ_KERNEL_QMM_NOWS = 4
 AQ_MATMUL_OVERLAP_PREVIOUS = 1
+AQ_FAULT_WAIT_MASK = 0x5F
 AQ_FAULT_BAD_INDEX = 0x20
 KERNELS = {"auto": AQ_KERNEL_AUTO, "qmv": AQ_KERNEL_QMV, "qmm": AQ_KERNEL_QMM, "qmv_tcgen05": AQ_KERNEL_QMV_TCGEN05,
            "qmm_nows": AQ_KERNEL_QMM_NOWS}
@@ -415,15 +416,15 @@ def aq_device_fault() -> int:
 
 
 def aq_set_wait_limit(cycles: int) -> None:
-    """Limit (SM clock cycles) of the decode kernel's bounded waits in later
-    launches; cycles <= 0 restores the default (about one second).  For tests
+    """Limit (SM clock cycles) of the bounded waits of the decode kernel and of
+    aq_kv_attention in later launches; cycles <= 0 restores the default (about one second).  For tests
     of the timeout path (see include/aq.h)."""
     lib().aq_set_wait_limit(int(cycles))
 
 
 def aq_set_wait_stall(on: bool) -> None:
-    """Make later decode-kernel launches wait on a barrier nothing completes, so
-    that their bounded wait runs out (a test of the timeout path; see include/aq.h)."""
+    """Make later launches of the decode kernel and of aq_kv_attention wait on a
+    barrier nothing completes, so that their bounded wait runs out (a test of the timeout path; see include/aq.h)."""
     lib().aq_set_wait_stall(1 if on else 0)
 
 

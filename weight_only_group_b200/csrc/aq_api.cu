@@ -91,6 +91,8 @@ namespace kv {
 cudaError_t read_and_clear_cache_fault(uint32_t *word);
 cudaError_t read_and_clear_attention_fault4(uint32_t *word);
 cudaError_t read_and_clear_attention_fault8(uint32_t *word);
+void set_wait_limit(long long cycles);
+void set_wait_stall(bool on);
 }  // namespace kv
 }  // namespace aq
 
@@ -277,11 +279,13 @@ int aq_last_cuda_error(void) { return t_last_cuda_error; }
 void aq_set_wait_limit(int64_t cycles) {
   aq::set_qmv_tc_wait_limit(static_cast<long long>(cycles));
   aq::set_qmv_umma_wait_limit(static_cast<long long>(cycles));
+  aq::kv::set_wait_limit(static_cast<long long>(cycles));
 }
 
 void aq_set_wait_stall(int on) {
   aq::set_qmv_tc_wait_stall(on != 0);
   aq::set_qmv_umma_wait_stall(on != 0);
+  aq::kv::set_wait_stall(on != 0);
 }
 
 aq_status aq_quantize(const float *w, int64_t N, int64_t K, int G, int bits, uint32_t *packed, uint16_t *scales,

@@ -18,7 +18,8 @@ namespace kv {
 constexpr int kTile = 16;  // tokens of a tile
 
 // Fault bits that these kernels raise: kFaultBadIndex for a page outside the cache or a position outside the table (zero
-// rows, or the tokens left out), kFaultQmvWait where attention gave up waiting for a tile.
+// rows, or the tokens left out), and their own bit where attention gave up waiting for a tile.
+constexpr uint32_t kFaultTileWait = 1u << 6;
 
 __host__ __device__ constexpr int row_bytes(int D, int bits) { return D * bits / 8; }
 __host__ __device__ constexpr int meta_bytes(int D, int G) { return 8 * (D / G); }
@@ -101,6 +102,8 @@ struct AttentionArgs {
   int window;           // 0: none
   float scale;
   void *workspace;
+  long long wait_cycles;  // limit of the waits for tiles
+  int stall;              // nonzero: every warp also waits on a barrier that nothing completes (timeout test)
 };
 
 cudaError_t launch_append(const AppendArgs &a, int D, int G, int bits, cudaStream_t s);

@@ -1,5 +1,6 @@
 // C ABI entry points of the quantised key-value cache: argument validation and
 // launches.  Layouts and method: see include/aq.h and kv.cuh.
+#include <atomic>
 #include <cmath>
 
 #include "kv.cuh"
@@ -7,6 +8,13 @@
 namespace aq {
 aq_status api_from_cuda(cudaError_t e);
 aq_status api_check_device();
+
+namespace kv {
+static std::atomic<long long> g_wait_limit{kWaitCycles};  // aq_set_wait_limit
+static std::atomic<bool> g_wait_stall{false};             // aq_set_wait_stall
+void set_wait_limit(long long cycles) { g_wait_limit.store(cycles > 0 ? cycles : kWaitCycles); }
+void set_wait_stall(bool on) { g_wait_stall.store(on); }
+}  // namespace kv
 }  // namespace aq
 
 namespace {
@@ -160,6 +168,8 @@ aq_status aq_kv_attention(const aq_kv_cache *cache, const uint16_t *q_bf16, int6
   a.lse = lse;
   a.scale = scale;
   a.workspace = workspace;
+  a.wait_cycles = aq::kv::g_wait_limit.load(std::memory_order_relaxed);
+  a.stall = aq::kv::g_wait_stall.load(std::memory_order_relaxed) ? 1 : 0;
   return aq::api_from_cuda(cache->bits == 4 ? aq::kv::launch_attention4(a, cache->D, cache->G, stream)
                                             : aq::kv::launch_attention8(a, cache->D, cache->G, stream));
 }

@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D
   using F = Form<BITS, D, G, ROWS>;
   constexpr int CT = F::kCT, CHUNK = CT * kTile, kWarps = F::kWarps, kThreads = F::kThreads, kUnitCost = F::kUnitCost;
   extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings
-  __shared__ uint64_t bars[kWarps][F::kStages];
+  __shared__ uint64_t bars[kWarps][F::kStages], stall_bar;  // (no thread ever arrives on the latter)
   __shared__ int sums[kThreads + 1], warp_sums[kWarps];
   __shared__ int head_unit[kWarps], tail_unit[kWarps], tail_first[kWarps], tail_end[kWarps];
   __shared__ bool tail_starts[kWarps];
@@ -783,7 +783,11 @@ __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D
     for (int i = 0; i < F::kStages; ++i) mbar_init(&bars[warp][i], 1);
     fence_barrier_init();
   }
-  if (threadIdx.x == 0) abort_flag = 0;
+  if (threadIdx.x == 0) {
+    mbar_init(&stall_bar, 1);
+    fence_barrier_init();
+    abort_flag = 0;
+  }
   await_previous();
   const int units = a.c.heads * plan.row_tiles;  // of a sequence
   Cursor<CHUNK> cur;
@@ -894,16 +898,16 @@ __global__ void __launch_bounds__(Form<BITS, D, G, ROWS>::kThreads, Form<BITS, D
     load_queries(queries, a, cur.seq, cur.head, cur.row_tile * ROWS);
     for (int i = 0; i < F::kStages && left > 0; ++i) issue();
     // --- the run, unit by unit
-    bool ok = true;
+    bool ok = !a.stall || __all_sync(0xffffffffu, mbar_wait(&stall_bar, 0, &abort_flag, &g_fault, kFaultTileWait, a.wait_cycles));
     int at = begin, stage = 0, parity = 0;
-    while (true) {
+    while (ok) {
       const int row0 = cur.row_tile * ROWS;
       const int first = cur.chunk, take = min(cur.span.chunks - first, end - at);
       State<BITS, D, G, ROWS> st;
       start_unit(st, queries, a, cur.span.len, row0);
       int pos = (cur.span.first + first) * CHUNK;
       for (int i = 0; i < take; ++i, pos += CHUNK) {
-        ok = mbar_wait(&bars[warp][stage], parity, &abort_flag, &g_fault, kFaultQmvWait);
+        ok = mbar_wait(&bars[warp][stage], parity, &abort_flag, &g_fault, kFaultTileWait, a.wait_cycles);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         run_chunk(st, a, ring + stage * F::kStage, pos, valid_bits & ((1u << CT) - 1u));
