@@ -609,13 +609,16 @@ def aq_kv_token_bytes(D: int, G: int, bits: int) -> int:
 
 def aq_kv_cache(pages: int, heads: int, page_size: int, D: int, G: int, bits: int, device="cuda") -> torch.Tensor:
     """A zeroed cache, uint8 [pages, heads, page_size, aq_kv_token_bytes(D, G, bits)].  A page of one head is laid out
-    in tiles of 16 tokens (include/aq.h), so the last two dimensions only count its bytes."""
+    in tiles of 16 tokens (include/aq.h), so the last two dimensions only count its bytes.  Forms of different D may have
+    the same number of bytes, so the tensor remembers its own and is refused for another; a view of it does not."""
     tb = aq_kv_token_bytes(D, G, bits)
     if tb == 0:
         raise AqError(AQ_ERR_UNSUPPORTED, "aq_kv_cache")
     if min(pages, heads, page_size) <= 0:
         raise ValueError("pages, heads and page_size must be positive")
-    return torch.zeros((pages, heads, page_size, tb), dtype=torch.uint8, device=device)
+    cache = torch.zeros((pages, heads, page_size, tb), dtype=torch.uint8, device=device)
+    cache._aq_kv_form = (D, G, bits)
+    return cache
 
 
 # (These calls are short and frequent: each check below is one attribute or method of a tensor, and none is made twice.)
@@ -648,6 +651,9 @@ def _kv(cache, table, lens, D: int, G: int, bits: int):
         if aq_kv_token_bytes(D, G, bits) == 0:
             raise AqError(AQ_ERR_UNSUPPORTED, "a key-value cache")
         raise ValueError(f"a token of the cache has {held} bytes, one of D = {D}, G = {G}, {bits} bits has {tb}")
+    form = getattr(cache, "_aq_kv_form", None)
+    if form is not None and form != (D, G, bits):
+        raise ValueError("the cache was made for D = {}, G = {}, {} bits".format(*form))
     return _KVCache(cache.data_ptr(), pages, heads, page_size, D, G, bits, tp, lp, batch, width), dev
 
 
