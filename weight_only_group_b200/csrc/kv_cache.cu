@@ -32,7 +32,7 @@ AQ_DEVICE bool locate(const Cache &c, const int32_t *offsets, int rows_per_seq, 
     // the last b with offsets[b] <= r, or 0: the lanes look at 32 entries at a time
     int lo = 0, n = c.batch;
     while (n > 1) {
-      const int step = (n + 31) >> 5, at = lane * step;
+      const int step = ((n - 1) >> 5) + 1, at = lane * step;
       const uint32_t below = __ballot_sync(0xffffffffu, at < n && load<int32_t>(offsets + lo + at) <= r) | 1u;
       const int k = 31 - __clz(below);
       lo += k * step;
