@@ -12,8 +12,9 @@
 // converted.  The nibble above counts 16 times, which q's fragment (K) and the
 // accumulator's rows (V) take back, both exactly.
 //
-// Bound: the cache's bytes, each read once.  A KV head's few query rows (4, 8 or
-// 16 at a time) make mma.sync m16n8k16 the right size: tokens (K) or dimensions (V)
+// Bound: the cache's bytes, each read once for a KV head's query rows up to 16 (8
+// at D = 256), and once more for every row tile beyond.  These few rows (4, 8 or 16
+// at a time) make mma.sync m16n8k16 the right size: tokens (K) or dimensions (V)
 // are its 16 rows, query rows its 8 columns.  A tcgen05 tile has 128 rows or more
 // and takes its operands from shared or tensor memory, so each code would be
 // unpacked into memory once more for work that is a few percent of the pipe.
@@ -49,8 +50,8 @@ constexpr int kSms = 148;         // the grid never has more CTAs than these hol
 constexpr int kMostCtas = 3;      // of an SM
 constexpr int kJoinThreads = 256;
 constexpr float kLowest = -FLT_MAX;  // the reference of a row that has seen nothing: below any score, and finite
-// Where units are no more than the GPU holds CTAs, and none can have more than this many bytes of cache for each warp of a
-// CTA (twice as many where there are enough units for nearly every SM), a CTA takes a unit: no list of places, no second
+// Where units are no more than the GPU holds CTAs, and none can have more (by the table's room or the window: lengths are not
+// known on the host) than this many bytes of cache for each warp of a CTA (twice as many where there are enough units for nearly every SM), a CTA takes a unit: no list of places, no second
 // kernel.  Measured against the list (4 bits, D = 128, four rows, 8 warps: 4 chunks of 32 tokens a warp are 1024 tokens): 8
 // to 256 units of 128 tokens 5.2 to 6.4 us against 9.3 to 11.4 us, of 1024 tokens 9.8 to 14.9 against 9.2 to 19.0 us; of 2048
 // tokens 14.7 against 9.2 us at 8 units, 14.9 against 13.5 us at 64, 15.9 against 18.2 us at 128.  Eight rows, 4 warps: 8
@@ -90,7 +91,8 @@ struct Form {
   static constexpr int kStages = 2;
   static constexpr int kRing = kStages * kStage;  // bytes of a warp's ring
   // Warps of a CTA and CTAs of an SM.  Four rows: 16 warps of 128 registers.  Eight rows, whose accumulators and queries take
-  // 24 more: 12 warps of 168.  8 warps of 255 where 16 rows' or wide heads' accumulators leave no room for more, and for
+  // 24 more: 12 warps of 168.  (Measured at G = 64; of the other groups at D = 128, four rows of 4 bits spill 9 to 14 registers,
+  // 16 rows of G = 32 two.)  8 warps of 255 where 16 rows' or wide heads' accumulators leave no room for more, and for
   // the tiles of 8 bits at D = 128, of which 8 warps keep enough in flight.  Measured: ragged, four rows 68.3 us at 16 warps and
   // 71.7 at 12; eight rows 80.2 at 16 and 75.2 at 12; 16 rows 107.9 in CTAs of 8 warps and 105.5 in CTAs of 4; 8 bits, D = 128,
   // eight rows 113.3 at 8 warps and 124.5 at 12.
